@@ -258,9 +258,9 @@ def prepare(case, seed):
     st["status"] = torch.zeros(8, dtype=torch.int32, device=DEV)
     if own:  # the handle of the cache and the scratch that a program keeps with it
         import moe_decode_megakernel_gb300 as mk
-        st["cache"] = mk.KvCache(st["k"], st["v"])
+        st["cache"] = mk.KvCache(st["k"], st["v"], ROPE_BASE)
         if case["op"] == "attn":
-            need = mk.tree_attn_workspace_bytes(st["cache"], case["n_q"], st["q"].shape[0])
+            need = mk.tree_attn_workspace_bytes(st["cache"])
             st["workspace"] = torch.empty(need, dtype=torch.uint8, device=DEV)
     return st
 
@@ -301,7 +301,7 @@ def _append(st):
     q, k, v = _split(st)
     if own:
         import moe_decode_megakernel_gb300 as mk
-        mk.kv_append(st["cache"], 0, k, v, st["cu"], st["ctx"], st["tables"], ROPE_BASE, q=q, q_out=st["q_out"],
+        mk.kv_append(st["cache"], 0, k, v, st["cu"], st["ctx"], st["tables"], q=q, q_out=st["q_out"],
                      positions=st["positions"], status=st["status"])
     else:
         b, i = _owner(st["cu"], q.shape[0])
