@@ -300,3 +300,8 @@ def weights_from(tensors: dict) -> MkWeights:
         t = tensors.get(k)
         return t.data_ptr() if t is not None else None
     return MkWeights(*[ptr(n) for n, _ in MkWeights._fields_])
+
+
+# the operators beside the decode step (include/mk_ops.h)
+from .ops import (KvCache, beam_reorder, beam_select, beam_select_workspace_bytes, check_status,  # noqa: E402
+                  kv_append, kv_commit, tree_attn, tree_attn_workspace_bytes)

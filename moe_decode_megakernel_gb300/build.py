@@ -11,7 +11,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["mk_api.cpp", "mk_sched.cpp", "mk_static_ws.cu", "mk_service.cpp", "mk_gpu_step.cu"]
+SOURCES = ["mk_api.cpp", "mk_sched.cpp", "mk_static_ws.cu", "mk_service.cpp", "mk_gpu_step.cu",
+           "ops/mk_kv_ops.cu", "ops/mk_beam.cu", "ops/mk_tree_attn.cu"]
 # the compiled model shapes (hidden, n_q, n_kv, head_dim, n_experts, top_k, inter,
 # page_size; the same table as kShapes in mk_api.cpp) and kernel modes (KernelMode):
 # mk_shape.cu is compiled once per pair
@@ -59,7 +60,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    units = [(src, [], os.path.splitext(src)[0]) for src in SOURCES]
+    units = [(src, [], os.path.splitext(os.path.basename(src))[0]) for src in SOURCES]
     for shape, dims in SHAPES.items():
         for mode in range(MODES):
             fn = f"launch_{shape}_{mode}"

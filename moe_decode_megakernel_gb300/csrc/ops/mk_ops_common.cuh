@@ -1,0 +1,129 @@
+// mk_ops_common.cuh -- what the operators of include/mk_ops.h share: the
+// handle on the pools, the status record, host checks, the ragged batch.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+#include <string>
+
+#include "../../../include/mk_ops.h"
+#include "../mk_host.h"
+#include "../mk_kernel.cuh"
+
+struct mk_kv {
+  mk_kv_config cfg;
+  int page_shift = 0;
+  // turns per position of each rotated pair, as a fraction of 2^64
+  uint64_t freq[64] = {};
+  // tensor maps of the pools, made by the first call that reads through them
+  std::mutex tm_lock;
+  bool tm_ready = false;
+  CUtensorMap tm_k, tm_v;
+};
+
+namespace mk {
+namespace ops {
+
+enum OpId : uint32_t { OP_APPEND = 1, OP_ATTN = 2, OP_COMMIT = 3, OP_REORDER = 4 };
+
+// The pools as the kernels see them.
+struct Pools {
+  uint16_t* k;  // of the call's first layer
+  uint16_t* v;
+  int64_t num_pages;
+  int64_t layer_elems;  // elements of one layer
+  int32_t n_kv, page_shift, n_layers;
+};
+
+struct Batch {
+  const int32_t* cu;
+  const int32_t* ctx;
+  const int32_t* tables;
+  const int32_t* positions;
+  int32_t batch, n_tokens, max_pages;
+};
+
+// The first record stays: {code, operator, row, index, value, limit}.
+__device__ inline void record(uint32_t* status, uint32_t code, uint32_t op, uint32_t row, uint32_t index, uint32_t value,
+                              uint32_t limit) {
+  if (!status || atomicCAS(status, 0u, code) != 0u) return;
+  status[1] = op;
+  status[2] = row;
+  status[3] = index;
+  status[4] = value;
+  status[5] = limit;
+}
+
+// Sequence b of a ragged batch: its rows [t0, t0 + n) and its cache length;
+// n = 0 (and the fault recorded) where the batch's numbers cannot be.
+struct Seq {
+  int t0, n, ctx;
+};
+__device__ inline Seq seq_of(const Batch& a, int b, int page_shift, uint32_t* status, uint32_t op) {
+  Seq s;
+  s.t0 = a.cu[b];
+  const int t1 = a.cu[b + 1];
+  s.ctx = a.ctx[b];
+  s.n = t1 - s.t0;
+  if (s.t0 < 0 || s.n < 0 || t1 > a.n_tokens) {
+    record(status, dev::ERR_INDEX, op, b, 0, t1, a.n_tokens);
+    s.n = 0;
+  } else if (s.n > 0 && (s.ctx < 0 || (int64_t)s.ctx + s.n > ((int64_t)a.max_pages << page_shift))) {
+    record(status, dev::ERR_RANGE, op, b, 1, s.ctx, a.max_pages << page_shift);
+    s.n = 0;
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------- host side
+inline bool misaligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an && bn && x < y + bn && y < x + an;
+}
+
+// Bytes of a strided token array: the last row counts its own elements only.
+inline size_t span(int64_t rows, int64_t stride, int64_t row_elems, size_t elem) {
+  return rows > 0 ? (size_t)((rows - 1) * stride + row_elems) * elem : 0;
+}
+
+inline int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+  return MK_OK;
+}
+
+inline Pools pools_of(const mk_kv* kv, int32_t layer) {
+  const mk_kv_config& c = kv->cfg;
+  Pools p;
+  p.layer_elems = c.num_pages * c.n_kv * c.page_size * c.head_dim;
+  p.k = static_cast<uint16_t*>(c.k_pool) + layer * p.layer_elems;
+  p.v = static_cast<uint16_t*>(c.v_pool) + layer * p.layer_elems;
+  p.num_pages = c.num_pages;
+  p.n_kv = c.n_kv;
+  p.page_shift = kv->page_shift;
+  p.n_layers = c.n_layers;
+  return p;
+}
+
+// The checks that append and attention share.
+inline int check_tokens(const mk_kv* kv, int32_t layer, const mk_tokens* t) {
+  if (!kv || !t) return fail(MK_ERR_ARG, "null argument");
+  if (layer < 0 || layer >= kv->cfg.n_layers) return fail(MK_ERR_ARG, "layer outside the pools");
+  if (t->batch < 0 || t->n_tokens < 0 || t->max_pages < 1) return fail(MK_ERR_ARG, "negative batch or token count, or no page columns");
+  if (((int64_t)t->max_pages << kv->page_shift) > INT32_MAX) return fail(MK_ERR_ARG, "block tables of more than 2^31 - 1 slots");
+  if (t->batch > 0 && (!t->cu_seqlens || !t->cache_lens || !t->block_tables)) return fail(MK_ERR_ARG, "null batch array");
+  return MK_OK;
+}
+
+inline Batch batch_of(const mk_tokens* t) {
+  return {t->cu_seqlens, t->cache_lens, t->block_tables, t->positions, t->batch, t->n_tokens, t->max_pages};
+}
+
+int encode_pools(mk_kv* kv);  // the handle's tensor maps, once
+
+}  // namespace ops
+}  // namespace mk
