@@ -1,12 +1,41 @@
 // mk_tree_attn.cu -- attention of new tokens (a drafted tree, or a run) over
-// the paged pools.
+// the paged pools, on the tcgen05 tensor cores.
+//
+// The work is cut into units: 128 slots of K and V of one (sequence, K/V head)
+// against one group of up to 256 query rows.  A query row is a (token, query
+// head) pair of the K/V head, in the order token * group + head, so that the
+// rows of a tree share each K/V tile that is read.  All units, in the order
+// (sequence, head, query group, tile), are dealt to the SMs in equal runs: a
+// long context is split over many SMs, a short one costs no more than it
+// holds, and nothing about the lengths is known to the host.  Where an item
+// (all tiles of one query group) is cut by the border between two SMs, each
+// leaves its part (row maxima, sums, unnormalised outputs, fp32) in the
+// workspace and a second kernel joins the parts in order.
+//
+// One CTA per SM, 12 warps:
+//   warp 0      producer: page ids from the block table, K and V tiles by TMA
+//               (one box per page and 64 dims, 128-byte swizzle) into a ring
+//   warp 1      one thread issues the MMAs: S = Q K^T (both from shared
+//               memory) and O += P V (P from tensor memory, V as it lies in
+//               the pages: the MMA takes its B operand with N contiguous)
+//   warps 2-3   in tiles that some row sees in part only: rows of V that lie
+//               behind the sequence, or hold an infinity or NaN, are zeroed
+//               before the MMA reads them (0 * NaN would reach every row)
+//   warps 4-11  two groups of 128 threads, a thread per query row: S from
+//               tensor memory, the running maximum and sum, P back as bf16
+// The two groups take the two halves of 256 query rows, or, where an item has
+// at most 128 rows, its even and odd tiles: one group's exponentials run under
+// the other's MMAs.
 #include <cmath>
 
 #include "mk_ops_common.cuh"
+#include "mk_ops_tmem.cuh"
 
 namespace mk {
 namespace ops {
 namespace {
+
+using namespace mk::dev;
 
 struct AttnArgs {
   Pools pools;
@@ -16,86 +45,873 @@ struct AttnArgs {
   float* lse;
   const uint64_t* mask;
   int64_t q_stride, out_stride;
-  int32_t n_q, group, mask_words, window;
-  float scale;
+  int32_t n_q, group, mask_words, window, layer;
+  float scale_log2;  // scale * log2(e)
+  float4* part_o;    // [2 * grid][D / 4][kRows]
+  float2* part_ml;   // [2 * grid][kRows]: maximum (log2 units), sum
   uint32_t* status;
+  CUtensorMap tm_k, tm_v;
 };
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128;               // slots of a K/V tile, rows of an MMA
+constexpr int kRows = 2 * kTile;         // query rows of an item
+constexpr int kThreads = 384;
+constexpr int kMaxItems = 16;            // items planned at a time
+constexpr float kSlack = 8.0f;           // log2: how far the maximum in use may lag
+constexpr int64_t kWaitNs = 2000000000;  // a wait that takes longer is given up
 
-// One block per (token, query head): each warp takes every fourth slot, a lane
-// D / 32 elements of the head.
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_simple(const __grid_constant__ AttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ int found;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid == 0) found = -1;
-  __syncthreads();
-  for (int b = tid; b < a.b.batch; b += kThreads)
-    if (a.b.cu[b] <= t && t < a.b.cu[b + 1]) found = b;
-  __syncthreads();
-  const int b = found;
-  if (b < 0) return;
+struct Geo {
+  static constexpr int kHalves = D / 64;           // 128-byte columns of a row
+  static constexpr int kHalfBytes = kTile * 128;   // a tile's 64 dims
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;  // K and V tiles in flight
+  static constexpr int kQ = 0, kRing = 2 * kTileBytes, kCtl = kRing + kStages * kTileBytes;
+};
+
+// One item as far as this CTA has to compute it.
+struct Item {
+  int b, h, t0, n, ctx;        // sequence, K/V head, its first token row, new tokens, cached
+  int row0, rows;              // query rows of the K/V head: first, count (1 .. kRows)
+  int lo, hi;                  // tiles of this part
+  int masked_from, window_to;  // tiles >= the one or < the other may be masked in part
+  int slot;                    // workspace slot of the part, -1: the item is whole
+};
+
+struct Ctl {
+  uint64_t full[8], empty[8], s_full[2], p_ready[2], o_full[2], v_go, v_ok, q_ready, rows_done, drain;
+  uint32_t tmem, abort;
+  int n_items, ok;
+  int64_t first, end;  // this CTA's units
+  int64_t next;
+  int bad_v[kMaxItems];  // an infinity or NaN was zeroed in one of the item's tiles
+  Item items[kMaxItems];
+  float2 ml[kTile];      // the second group's maxima and sums
+};
+
+// ------------------------------------------------------------- the plan
+
+__device__ __forceinline__ Seq attn_seq(const AttnArgs& a, int b) {
   Seq s = seq_of(a.b, b, a.pools.page_shift, a.status, OP_ATTN);
-  if (a.mask && s.n > 64 * a.mask_words) {
-    record(a.status, dev::ERR_RANGE, OP_ATTN, b, 2, s.n, 64 * a.mask_words);
+  if (a.mask && s.n > 64 * (int64_t)a.mask_words) {
+    record(a.status, ERR_RANGE, OP_ATTN, b, 2, s.n, 64 * a.mask_words);
     s.n = 0;
   }
-  if (s.n == 0) return;
-  const int i = t - s.t0, g = h / a.group, P = 1 << a.pools.page_shift;
-  auto position = [&](int j) {
-    const int slot = s.ctx + j;
-    if (!a.b.positions) return slot;
-    const int p = a.b.positions[s.t0 + j];
-    if (p < s.ctx || p >= s.ctx + s.n) {
-      if (a.window) record(a.status, dev::ERR_RANGE, OP_ATTN, b, 3, p, s.ctx + s.n);
-      return p < s.ctx ? s.ctx : s.ctx + s.n - 1;
-    }
-    return p;
-  };
-  const int pos = a.window ? position(i) : 0;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0;
-  for (int e = 0; e < E; ++e)
-    q[e] = a.scale * __uint_as_float((uint32_t)a.q[t * a.q_stride + h * D + lane * E + e] << 16);
-  const int end = s.ctx + s.n;
-  for (int slot = warp; slot < end; slot += 4) {
-    const int j = slot - s.ctx;
-    bool see = true;
-    if (j >= 0) see = a.mask ? (a.mask[(int64_t)t * a.mask_words + j / 64] >> (j % 64)) & 1 : j <= i;
-    if (a.window) see = see && pos - (j >= 0 ? position(j) : slot) < a.window;
-    if (!see) continue;
-    int64_t page = a.b.tables[(int64_t)b * a.b.max_pages + (slot >> a.pools.page_shift)];
-    if (page < 0 || page >= a.pools.num_pages) {
-      record(a.status, dev::ERR_PAGE, OP_ATTN, b, slot, (uint32_t)page, (uint32_t)a.pools.num_pages);
-      page = 0;
-    }
-    const int64_t row = ((page * a.pools.n_kv + g) << a.pools.page_shift) + (slot & (P - 1));
-    float d = 0;
-    for (int e = 0; e < E; ++e) d += q[e] * __uint_as_float((uint32_t)a.pools.k[row * D + lane * E + e] << 16);
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    const float mn = fmaxf(m, d), z = mn == -INFINITY ? 0.0f : mn;
-    const float c = expf(m - z), p = expf(d - z);
-    l = l * c + p;
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * c + p * __uint_as_float((uint32_t)a.pools.v[row * D + lane * E + e] << 16);
-    m = mn;
+  return s;
+}
+
+// Tiles [lo, hi) of query group m of a sequence.
+__device__ __forceinline__ void tiles_of(const AttnArgs& a, const Seq& s, int m, int& lo, int& hi) {
+  const int64_t all = (int64_t)s.n * a.group, r0 = (int64_t)m * kRows, r1 = r0 + kRows < all ? r0 + kRows : all;
+  const int i0 = (int)(r0 / a.group), i1 = (int)((r1 - 1) / a.group);
+  const int end = s.ctx + (a.mask ? s.n : i1 + 1);
+  hi = (end + kTile - 1) / kTile;
+  lo = 0;
+  if (a.window) {
+    const int first = s.ctx + (a.b.positions ? 0 : i0) - a.window + 1;  // the lowest slot that a row sees
+    if (first > 0) lo = first / kTile;
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+}
+
+__device__ __forceinline__ int groups_of(const AttnArgs& a, const Seq& s) {
+  return (int)(((int64_t)s.n * a.group + kRows - 1) / kRows);
+}
+
+// Units of one K/V head of a sequence.
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Seq& s) {
+  int64_t u = 0;
+  for (int m = 0, M = groups_of(a, s); m < M; ++m) {
+    int lo, hi;
+    tiles_of(a, s, m, lo, hi);
+    u += hi - lo;
+  }
+  return u;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t w = __shfl_up_sync(FULL, v, o);
+    if ((int)(threadIdx.x % 32) >= o) v += w;
+  }
+  return v;
+}
+
+// All units (by one warp).
+__device__ int64_t total_units(const AttnArgs& a) {
+  int64_t u = 0;
+  for (int b = threadIdx.x % 32; b < a.b.batch; b += 32) u += units_of(a, attn_seq(a, b)) * a.pools.n_kv;
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
+  return u;
+}
+
+__device__ __forceinline__ int64_t border(int64_t total, int c, int grid) { return total * c / grid; }
+
+// The item of unit u at (h, m) of sequence b, whose units of this head begin
+// at unit `base`: everything but the part.
+__device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b, int h, int m) {
+  Item it;
+  it.b = b, it.h = h, it.t0 = s.t0, it.n = s.n, it.ctx = s.ctx;
+  const int64_t all = (int64_t)s.n * a.group;
+  it.row0 = m * kRows;
+  it.rows = all - it.row0 < kRows ? (int)(all - it.row0) : kRows;
+  tiles_of(a, s, m, it.lo, it.hi);
+  const int i0 = it.row0 / a.group, i1 = (it.row0 + it.rows - 1) / a.group;
+  it.masked_from = (s.ctx + (a.mask ? 0 : i0 + 1)) / kTile;
+  it.window_to = 0;
+  if (a.window) {
+    const int first = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
+    if (first > 0) it.window_to = (first + kTile - 1) / kTile;
+  }
+  it.slot = -1;
+  return it;
+}
+
+// Calls f(item, first unit of the item) for the items that hold units [u, end),
+// in order, while it returns true.  By one warp; f runs on every lane.
+template <typename F>
+__device__ void each_item(const AttnArgs& a, int64_t u, int64_t end, F f) {
+  const int lane = threadIdx.x % 32;
+  int64_t base = 0;  // units before this round of sequences
+  for (int b0 = 0; b0 < a.b.batch && base < end; b0 += 32) {
+    Seq s = {0, 0, 0};
+    int64_t per_head = 0;
+    if (b0 + lane < a.b.batch) {
+      s = attn_seq(a, b0 + lane);
+      per_head = units_of(a, s);
+    }
+    const int64_t incl = warp_scan(per_head * a.pools.n_kv);
+    uint32_t hit = __ballot_sync(FULL, per_head > 0 && base + incl > u && base + incl - per_head * a.pools.n_kv < end);
+    while (hit) {
+      const int src = __ffs(hit) - 1;
+      hit &= hit - 1;
+      const Seq q = {__shfl_sync(FULL, s.t0, src), __shfl_sync(FULL, s.n, src), __shfl_sync(FULL, s.ctx, src)};
+      const int64_t ph = __shfl_sync(FULL, per_head, src), begin = base + __shfl_sync(FULL, incl, src) - ph * a.pools.n_kv;
+      const int M = groups_of(a, q);
+      int h = u > begin ? (int)((u - begin) / ph) : 0;
+      for (; h < a.pools.n_kv; ++h) {
+        int64_t at = begin + h * ph;
+        if (at >= end) return;
+        for (int m = 0; m < M; ++m) {
+          int lo, hi;
+          tiles_of(a, q, m, lo, hi);
+          if (at + (hi - lo) > u) {
+            if (at >= end) return;
+            if (!f(make_item(a, q, b0 + src, h, m), at)) return;
+          }
+          at += hi - lo;
+        }
+      }
+    }
+    base += __shfl_sync(FULL, incl, 31);
+  }
+}
+
+// ------------------------------------------------------------- waits
+
+// Waits for a phase; false when this wait, or another one of the CTA, has
+// taken too long.
+__device__ __noinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
+  const int64_t until = gtimer() + kWaitNs;
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (ld_volatile(&c.abort)) return false;
+    if (gtimer() > until) {
+      *reinterpret_cast<volatile uint32_t*>(&c.abort) = 1;
+      record(status, ERR_TIMEOUT, OP_ATTN, blockIdx.x, threadIdx.x, 0, 0);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, status);
+}
+
+// A ring position: stage and phase of the k-th tile.
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  template <int N>
+  __device__ __forceinline__ void advance() {
+    if (++stage == N) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ bool both_in(const Item& it) { return it.rows > kTile; }
+__device__ __forceinline__ bool in_part(const Item& it, int j) { return j >= it.masked_from || j < it.window_to; }
+
+// ------------------------------------------------------------- visibility
+
+// Bits of the new tokens j0 .. j0 + 31 in a token's mask row (j0 > -32; bits
+// below token 0 are clear).
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* row, int words, int j0) {
+  if (j0 < 0) return (uint32_t)(row[0] << -j0);
+  const int w = j0 >> 6, sh = j0 & 63;
+  uint64_t v = w < words ? row[w] >> sh : 0;
+  if (sh > 32 && w + 1 < words) v |= row[w + 1] << (64 - sh);
+  return (uint32_t)v;
+}
+
+// Position of new token j (a position out of range is moved into it).
+__device__ __forceinline__ int position_of(const AttnArgs& a, const Item& it, int j) {
+  if (!a.b.positions) return it.ctx + j;
+  const int p = a.b.positions[it.t0 + j];
+  if (p < it.ctx || p >= it.ctx + it.n) {
+    record(a.status, ERR_RANGE, OP_ATTN, it.b, 3, p, it.ctx + it.n);
+    return p < it.ctx ? it.ctx : it.ctx + it.n - 1;
+  }
+  return p;
+}
+
+// Which of the slots s0 .. s0 + 31 token i sees.
+__device__ __forceinline__ uint32_t seen(const AttnArgs& a, const Item& it, int i, int pos, int s0) {
+  const int len = it.ctx + it.n;
+  if (s0 >= len) return 0;
+  uint32_t v = FULL;
+  if (len - s0 < 32) v = FULL >> (32 - (len - s0));
+  const int j0 = s0 - it.ctx;
+  if (j0 > -32) {
+    uint32_t d;
+    if (a.mask) {
+      d = mask_bits(a.mask + (int64_t)(it.t0 + i) * a.mask_words, a.mask_words, j0);
+      if (j0 < 0) d |= (1u << -j0) - 1;
+    } else {
+      const int k = i + 1 - j0;  // tokens from j0 up to i
+      d = k <= 0 ? 0 : k >= 32 ? FULL : (1u << k) - 1;
+    }
+    v &= d;
+  }
+  if (a.window) {
+    const int first = pos - a.window + 1 - s0;  // cached slots (and a run's tokens) below it are out
+    uint32_t in = first <= 0 ? FULL : first >= 32 ? 0 : FULL << first;
+    if (a.b.positions && j0 > -32) {
+      const uint32_t fresh = j0 >= 0 ? FULL : FULL << -j0;
+      uint32_t near = fresh;
+      if (it.n > a.window)  // else no two new tokens are a window apart
+        for (uint32_t w = v & fresh; w; w &= w - 1) {
+          const int k = __ffs(w) - 1;
+          if (pos - position_of(a, it, j0 + k) >= a.window) near &= ~(1u << k);
+        }
+      in = (in & ~fresh) | near;
+    }
+    v &= in;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int64_t pool_row(const AttnArgs& a, const Item& it, int slot) {
+  int64_t page = a.b.tables[(int64_t)it.b * a.b.max_pages + (slot >> a.pools.page_shift)];
+  if (page < 0 || page >= a.pools.num_pages) page = 0;
+  return ((page * a.pools.n_kv + it.h) << a.pools.page_shift) + (slot & ((1 << a.pools.page_shift) - 1));
+}
+
+// ------------------------------------------------------------- roles
+
+template <int D>
+__device__ bool produce(const AttnArgs& a, uint8_t* smem, Ctl& c, Ring& r, uint32_t& filled) {
+  using G = Geo<D>;
+  const int lane = threadIdx.x % 32;
+  const int P = 1 << a.pools.page_shift, box = P < kTile ? P : kTile;  // slots of a box
+  const int slice = lane / G::kHalves, half = lane % G::kHalves;       // this lane's box of a tile
+  for (int k = 0; k < c.n_items; ++k) {
+    const Item it = c.items[k];
+    const int len = it.ctx + it.n;
+    const int32_t* table = a.b.tables + (int64_t)it.b * a.b.max_pages;
+    auto page_at = [&](int j) {  // the page of this lane's box in tile j, -1: no slot of it is in use
+      const int s = j * kTile + slice * box;
+      if (slice * box >= kTile || s >= len) return -1;
+      int page = table[s >> a.pools.page_shift];
+      if (page < 0 || page >= a.pools.num_pages) {
+        record(a.status, ERR_PAGE, OP_ATTN, it.b, s, page, (uint32_t)a.pools.num_pages);
+        page = 0;
+      }
+      return page;
+    };
+    int page = page_at(it.lo);
+    for (int j = it.lo; j < it.hi; ++j) {
+      const int next = j + 1 < it.hi ? page_at(j + 1) : -1;
+      const uint32_t bytes = __popc(__ballot_sync(FULL, page >= 0)) * box * 128;
+      const int y = ((page * a.pools.n_kv + it.h) << a.pools.page_shift) + ((j * kTile + slice * box) & (P - 1));
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        // the tile before last in this stage has been read
+        const bool ok = filled < (uint32_t)G::kStages || wait(c, &c.empty[r.stage], r.phase ^ 1, a.status);
+        if (!__all_sync(FULL, ok)) return false;
+        if (lane == 0) mbar_expect_tx(&c.full[r.stage], bytes);
+        __syncwarp();
+        if (page >= 0) {
+          uint8_t* dst = smem + G::kRing + r.stage * G::kTileBytes + half * G::kHalfBytes + slice * box * 128;
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+              " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+              "l"(reinterpret_cast<uint64_t>(kv ? &a.tm_v : &a.tm_k)), "r"(half * 64), "r"(y), "r"(a.layer),
+              "r"(smem_u32(&c.full[r.stage]))
+              : "memory");
+        }
+        ++filled;
+        r.advance<G::kStages>();
+      }
+      page = next;
+    }
+  }
+  return true;
+}
+
+// B operand with N contiguous (V as the pages hold it): 64-dim columns of
+// 128-byte rows, a K group of 8 slots every 1024 bytes, the next 64 dims a
+// half tile further.
+__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t half_bytes) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(half_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+struct MmaState {
+  Ring k;                        // the next K or V tile of the ring
+  uint32_t p_phase[2] = {0, 0};  // of p_ready
+  uint32_t q_phase = 0, v_phase = 0;  // of q_ready, of v_ok
+};
+
+template <int D>
+__device__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st) {
+  using G = Geo<D>;
+  constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kTile);
+  constexpr uint32_t idesc_o = tc_idesc_bf16(kTile, D) | (1u << 16);  // B with N contiguous
+  const uint32_t base = smem_u32(smem), tmem = c.tmem;
+  for (int k = 0; k < c.n_items; ++k) {
+    const Item it = c.items[k];
+    const bool both = both_in(it);
+    const int steps = (it.hi - it.lo) << (both ? 1 : 0);
+    // tile x of the item: K at ring position 2x, V at 2x + 1 from here on
+    Ring kpos = st.k, vpos = st.k;
+    vpos.advance<G::kStages>();
+    if (!wait(c, &c.q_ready, st.q_phase, a.status)) return false;
+    st.q_phase ^= 1;
+    tc_fence_after();
+    for (int s = -2; s < steps; ++s) {
+      if (s >= 0) {  // O += P V of step s
+        const int w = s & 1;
+        const bool first = s < 2, fresh = !both || w == 0, part = fresh && in_part(it, it.lo + (both ? s >> 1 : s));
+        // This thread waits for every tile of the ring, in order (a barrier's
+        // parity tells neighbouring phases apart, not those two laps apart),
+        // and sends the tiles that need it to clean_v.
+        if (fresh && !wait(c, &c.full[vpos.stage], vpos.phase, a.status)) return false;
+        if (part) mbar_arrive(&c.v_go);
+        if (!wait(c, &c.p_ready[w], st.p_phase[w], a.status)) return false;
+        st.p_phase[w] ^= 1;
+        if (part) {
+          if (!wait(c, &c.v_ok, st.v_phase, a.status)) return false;
+          st.v_phase ^= 1;
+        }
+        tc_fence_after();
+        const uint64_t vd = desc_v(base + G::kRing + vpos.stage * G::kTileBytes, G::kHalfBytes);
+#pragma unroll
+        for (int x = 0; x < kTile / 16; ++x)  // 16 slots: 8 columns of P, two 1024-byte groups of V
+          mma_bf16_ta(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * (2048 >> 4), idesc_o, !first || x > 0);
+        if (!both || w == 1) {
+          tc_commit(&c.empty[vpos.stage]);
+          vpos.advance<G::kStages>();
+          vpos.advance<G::kStages>();
+        }
+        if (s + 2 >= steps) {  // the group's last: its arrival carries what this thread has seen, the commit the MMAs
+          mbar_arrive(&c.o_full[w]);
+          tc_commit(&c.o_full[w]);
+        }
+      }
+      if (s + 2 < steps) {  // S = Q K^T of step s + 2
+        const int w = s & 1;
+        if ((!both || w == 0) && !wait(c, &c.full[kpos.stage], kpos.phase, a.status)) return false;
+        tc_fence_after();
+        const uint32_t qa = base + G::kQ + (both ? w * G::kTileBytes : 0), ka = base + G::kRing + kpos.stage * G::kTileBytes;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = x / 4 * G::kHalfBytes + x % 4 * 32;
+          tc_mma_bf16(tmem + w * 128, tc_desc_sw128(qa + off), tc_desc_sw128(ka + off), idesc_s, x > 0);
+        }
+        if (!both || w == 1) {
+          tc_commit(&c.empty[kpos.stage]);
+          kpos.advance<G::kStages>();
+          kpos.advance<G::kStages>();
+        }
+        tc_commit(&c.s_full[w]);
+      }
+    }
+    st.k = kpos;  // two positions per tile: behind the item's last V
+  }
+  return true;
+}
+
+// Rows of a partly masked tile's V that must not reach the MMA.
+struct CleanState {
+  Ring k;
+  uint32_t phase = 0;  // of v_go
+};
+
+template <int D>
+__device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st) {
+  using G = Geo<D>;
+  const int tid = threadIdx.x - 64;
+  for (int k = 0; k < c.n_items; ++k) {
+    const Item it = c.items[k];
+    for (int j = it.lo; j < it.hi; ++j) {
+      st.k.advance<G::kStages>();  // K
+      if (in_part(it, j)) {
+        if (!__all_sync(FULL, wait(c, &c.v_go, st.phase, a.status))) return false;
+        st.phase ^= 1;
+        const uint32_t tile = smem_u32(smem + G::kRing + st.k.stage * G::kTileBytes);
+        for (int row = tid; row < kTile; row += 64) {
+          bool drop = j * kTile + row >= it.ctx + it.n;
+          if (!drop) {
+            uint32_t odd = 0;  // exponents all ones
+            for (int ch = 0; ch < D / 8; ++ch) {
+              const uint4 u = lds128(tile + ch / 8 * G::kHalfBytes + row * 128 + ((ch % 8) ^ (row & 7)) * 16);
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                odd |= ((w[e] & 0x7f80u) == 0x7f80u) | ((w[e] & 0x7f800000u) == 0x7f800000u);
+            }
+            if (odd) {
+              drop = true;
+              *reinterpret_cast<volatile int*>(&c.bad_v[k]) = 1;
+            }
+          }
+          if (drop)
+            for (int ch = 0; ch < D / 8; ++ch)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + ch / 8 * G::kHalfBytes + row * 128 + ch % 8 * 16),
+                           "r"(0u)
+                           : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (tid % 32 == 0) mbar_arrive(&c.v_ok);
+      }
+      st.k.advance<G::kStages>();  // V
+    }
+  }
+  return true;
+}
+
+struct RowState {
+  uint32_t s_phase = 0, o_phase = 0, done_phase = 0;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What clean_v zeroed, for the rows that see it: its products with the row's
+// probabilities, added to 32 columns of the row's output.
+template <int D>
+__device__ __noinline__ void add_odd_v(const AttnArgs& a, const Item& it, int i, int g, int pos, float m, int col, float (&o)[32]) {
+  const uint16_t* q = a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D;
+  for (int j = it.lo; j < it.hi; ++j) {
+    if (!in_part(it, j)) continue;
+    for (int s = j * kTile; s < min((j + 1) * kTile, it.ctx + it.n); ++s) {
+      if (!(seen(a, it, i, pos, s) & 1)) continue;
+      const int64_t row = pool_row(a, it, s) * D;
+      bool odd = false;
+      float dot = 0;
+      for (int e = 0; e < D; ++e) {
+        odd |= (a.pools.v[row + e] & 0x7f80) == 0x7f80;
+        dot += __uint_as_float((uint32_t)q[e] << 16) * __uint_as_float((uint32_t)a.pools.k[row + e] << 16);
+      }
+      if (!odd) continue;
+      const float p = ex2(dot * a.scale_log2 - (m == -INFINITY ? 0.0f : m));
+      for (int e = 0; e < 32; ++e) o[e] += p * __uint_as_float((uint32_t)a.pools.v[row + col + e] << 16);
+    }
+  }
+}
+
+template <int D>
+__device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState& st) {
+  using G = Geo<D>;
+  const int tid = threadIdx.x - 128, w = tid / 128, r = tid % 128;
+  const uint32_t lane_base = c.tmem + ((uint32_t)(r / 32 * 32) << 16);
+  const uint32_t t_s = lane_base + w * 128, t_o = lane_base + 256 + w * 128;
+  for (int k = 0; k < c.n_items; ++k) {
+    const Item& it = c.items[k];
+    const bool both = both_in(it);
+    // Q: 16-byte chunks of the item's rows, into the MMA's K-major layout
+    const int q_rows = both ? kRows : kTile;
+    for (int x = tid; x < q_rows * (D / 8); x += 256) {
+      const int row = x / (D / 8), ch = x % (D / 8);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < it.rows) {
+        const int f = it.row0 + row, i = f / a.group, g = f % a.group;
+        u = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D) + ch);
+      }
+      const int rr = row % kTile;
+      uint8_t* dst = smem + G::kQ + row / kTile * G::kTileBytes + ch / 8 * G::kHalfBytes + rr * 128 + ((ch % 8) ^ (rr & 7)) * 16;
+      *reinterpret_cast<uint4*>(dst) = u;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&c.q_ready);
+
+    const int local = both ? w * kTile + r : r;  // row of the item
+    const bool mine = local < it.rows;
+    const bool warp_mine = (both ? w * kTile : 0) + r / 32 * 32 < it.rows;
+    const int f = it.row0 + (mine ? local : 0), i = f / a.group, g = f % a.group;
+    const int pos = a.window ? position_of(a, it, i) : 0;
+    float m = -INFINITY, l = 0.0f;
+    const int j0 = it.lo + (both ? 0 : w), dj = both ? 1 : 2, hi = it.hi, masked_from = it.masked_from, window_to = it.window_to;
+    for (int j = j0; j < hi; j += dj) {
+      if (!__all_sync(FULL, wait(c, &c.s_full[w], st.s_phase, a.status))) return false;
+      st.s_phase ^= 1;
+      if (!warp_mine) {  // no row of this warp: P's lanes are never used
+        mbar_arrive(&c.p_ready[w]);
+        continue;
+      }
+      tc_fence_after();
+      uint32_t s[128];
+      tmem_load(t_s, s);
+      if (j >= masked_from || j < window_to) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t v = seen(a, it, i, pos, j * kTile + x * 32);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((v >> e) & 1)) s[x * 32 + e] = 0xff800000u;
+        }
+      }
+      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 128; e += 8) {
+        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+        t2 = fmaxf(t2, fmaxf(__uint_as_float(s[e + 4]), __uint_as_float(s[e + 5])));
+        t3 = fmaxf(t3, fmaxf(__uint_as_float(s[e + 6]), __uint_as_float(s[e + 7])));
+      }
+      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
+      // The maximum in use may lag by kSlack (p <= 2^8, exact enough in bf16
+      // and fp32): the output is rescaled only where it lags further.
+      const bool up = top > m + kSlack;
+      if (__any_sync(FULL, up)) {
+        const float to = up ? top : m, by = up ? ex2(m - to) : 1.0f;
+        if (j != j0) {  // S of this step is ready, so P V of the one before is done
+#pragma unroll
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            tmem_load(t_o + x, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+            tmem_store(t_o + x, o);
+          }
+        }
+        l *= by;
+        m = to;
+      }
+      const float z = m == -INFINITY ? 0.0f : m;
+      float l0 = 0, l1 = 0, l2 = 0, l3 = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const uint32_t* x = s + half * 64 + e;
+          const float p0 = ex2(fmaf(__uint_as_float(x[0]), a.scale_log2, -z)), p1 = ex2(fmaf(__uint_as_float(x[1]), a.scale_log2, -z));
+          const float p2 = ex2(fmaf(__uint_as_float(x[2]), a.scale_log2, -z)), p3 = ex2(fmaf(__uint_as_float(x[3]), a.scale_log2, -z));
+          l0 += p0, l1 += p1, l2 += p2, l3 += p3;
+          p[e / 2] = pack_bf16(p0, p1);
+          p[e / 2 + 1] = pack_bf16(p2, p3);
+        }
+        tmem_store(t_s + half * 32, p);
+      }
+      l += (l0 + l1) + (l2 + l3);
+      tmem_store_wait();
+      tc_fence_before();
+      mbar_arrive(&c.p_ready[w]);
+    }
+
+    // the output
+    const bool any = j0 < hi;
+    if (any) {
+      if (!__all_sync(FULL, wait(c, &c.o_full[w], st.o_phase, a.status))) return false;
+      st.o_phase ^= 1;
+      tc_fence_after();
+    }
+    const bool join = !both && hi - it.lo > 1;  // the odd tiles' sums to the first group, through Q's place
+    float* other = reinterpret_cast<float*>(smem + G::kQ);
+    auto groups_meet = [&]() {
+      mbar_arrive(&c.rows_done);
+      const bool ok = __all_sync(FULL, wait(c, &c.rows_done, st.done_phase, a.status));
+      st.done_phase ^= 1;
+      return ok;
+    };
+    float f0 = 1.0f, f1 = 0.0f;
+    if (join) {
+      if (!groups_meet()) return false;  // no MMA reads Q any more
+      if (w == 1) {
+        if (warp_mine) {
+#pragma unroll
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            tmem_load(t_o + x, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) other[(x + e) * kTile + r] = __uint_as_float(o[e]);
+          }
+        }
+        c.ml[r] = make_float2(m, l);
+      }
+      if (!groups_meet()) return false;
+      if (w == 0) {
+        const float2 ml = c.ml[r];
+        const float top = fmaxf(m, ml.x), z = top == -INFINITY ? 0.0f : top;
+        f0 = ex2(m - z), f1 = ex2(ml.x - z);
+        m = top;
+        l = l * f0 + ml.y * f1;
+      }
+    }
+    const bool odd = *reinterpret_cast<volatile int*>(&c.bad_v[k]) != 0;
+    if (warp_mine && (both || w == 0)) {
+      const float inv = it.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* dst = a.out + (int64_t)(it.t0 + i) * a.out_stride + (int64_t)(it.h * a.group + g) * D;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        uint32_t u[32];
+        tmem_load(t_o + x, u);
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f0;
+        if (join) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] += other[(x + e) * kTile + r] * f1;
+        }
+        if (odd && mine) add_odd_v<D>(a, it, i, g, pos, m, x, o);
+        if (mine && it.slot >= 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            a.part_o[((int64_t)it.slot * (D / 4) + (x + e) / 4) * kRows + local] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (mine) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 v;
+            v.x = pack_bf16(o[e] * inv, o[e + 1] * inv), v.y = pack_bf16(o[e + 2] * inv, o[e + 3] * inv);
+            v.z = pack_bf16(o[e + 4] * inv, o[e + 5] * inv), v.w = pack_bf16(o[e + 6] * inv, o[e + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + x + e) = v;
+          }
+        }
+      }
+      if (mine) {
+        if (it.slot >= 0)
+          a.part_ml[(int64_t)it.slot * kRows + local] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[(int64_t)(it.t0 + i) * a.n_q + it.h * a.group + g] = (m + log2f(l)) * 0.693147180559945309f;
+      }
+    }
+    tc_fence_before();
+    if (!groups_meet()) return false;  // Q and the outputs may be overwritten
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+  using G = Geo<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl& c = *reinterpret_cast<Ctl*>(smem + G::kCtl);
+  const int tid = threadIdx.x, warp = tid / 32;
+  if (warp == 0) {
+    const int64_t total = total_units(a);
+    if (tid == 0) {
+      c.first = border(total, blockIdx.x, gridDim.x);
+      c.end = border(total, blockIdx.x + 1, gridDim.x);
+    }
+  }
+  if (tid == 0) {
+    c.ok = (smem_u32(smem) & 1023) == 0;
+    if (!c.ok) record(a.status, ERR_SMEM_ALIGN, OP_ATTN, 0, 0, smem_u32(smem), 1024);
+    c.abort = 0;
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&c.full[i], 1);
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_ready[i], 128);
+      mbar_init(&c.o_full[i], 2);
+    }
+    mbar_init(&c.v_go, 1);
+    mbar_init(&c.v_ok, 2);
+    mbar_init(&c.q_ready, 256);
+    mbar_init(&c.rows_done, 256);
+    mbar_init(&c.drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
-  float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])), L = 0;
-  const float z = M == -INFINITY ? 0.0f : M;
-  for (int w = 0; w < 4; ++w) L += sl[w] * expf(sm[w] - z);
-  for (int e = tid; e < D; e += kThreads) {
-    float x = 0;
-    for (int w = 0; w < 4; ++w) x += so[w][e] * expf(sm[w] - z);
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(L == 0 ? 0.0f : x / L));
-    a.out[t * a.out_stride + h * D + e] = (uint16_t)r;
+  int64_t u = c.first;
+  const int64_t begin = u, end = c.end;
+  if (u >= end || !c.ok) return;
+  if (warp == 1) tmem_alloc(&c.tmem, 512);
+  __syncthreads();
+
+  Ring fill;
+  CleanState check;
+  MmaState mma;
+  RowState rows;
+  uint32_t filled = 0;
+  bool ok = true;
+  while (u < end && ok) {
+    if (warp == 0) {  // the next items of this CTA's run of units
+      int n = 0;
+      int64_t next = end;
+      each_item(a, u, end, [&](Item it, int64_t at) {
+        if (n == kMaxItems) {
+          next = at;
+          return false;
+        }
+        const int64_t stop = at + (it.hi - it.lo);
+        const int64_t from = at < begin ? begin : at, to = stop < end ? stop : end;
+        // a part that begins its item is the run's last, any other its first
+        if (from > at)
+          it.slot = 2 * blockIdx.x;
+        else if (to < stop)
+          it.slot = 2 * blockIdx.x + 1;
+        it.hi = it.lo + (int)(to - at);
+        it.lo += (int)(from - at);
+        if (tid == 0) {
+          c.items[n] = it;
+          c.bad_v[n] = 0;
+        }
+        ++n;
+        return true;
+      });
+      if (tid == 0) {
+        c.n_items = n;
+        c.next = next;
+      }
+    }
+    __syncthreads();
+    if (warp == 0)
+      ok = produce<D>(a, smem, c, fill, filled);
+    else if (tid == 32)
+      ok = issue_mmas<D>(a, smem, c, mma);
+    else if (warp == 2 || warp == 3)
+      ok = clean_v<D>(a, smem, c, check);
+    else if (warp >= 4)
+      ok = softmax_rows<D>(a, smem, c, rows);
+    ok = __syncthreads_and(ok);
+    u = c.next;
+    __syncthreads();
   }
-  if (a.lse && tid == 0) a.lse[(int64_t)t * a.n_q + h] = M + logf(L);
+  if (!ok) {
+    // a wait was given up: the copies and MMAs in flight first (bounded)
+    if (tid == 0) {
+      Ring r = fill;
+      for (uint32_t i = 0; i < (uint32_t)G::kStages && i < filled; ++i) {  // the last fill of every stage
+        r.stage = r.stage == 0 ? G::kStages - 1 : r.stage - 1;
+        if (r.stage == G::kStages - 1) r.phase ^= 1;
+        for (int64_t until = gtimer() + kWaitNs; !mbar_try_wait(&c.full[r.stage], r.phase) && gtimer() < until;) {
+        }
+      }
+    }
+    if (tid == 32) {
+      tc_commit(&c.drain);
+      for (int64_t until = gtimer() + kWaitNs; !mbar_try_wait(&c.drain, 0) && gtimer() < until;) {
+      }
+    }
+    __syncthreads();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_dealloc(c.tmem, 512);
+}
+
+// ------------------------------------------------------------- the join
+
+constexpr int kJoinRows = 32, kJoinThreads = 256, kMaxGrid = 160;
+
+// Block (c - 1, y): if the border between CTAs c - 1 and c of the first kernel
+// is the first one inside an item, joins 32 of that item's rows: the parts of
+// CTAs c - 1, c, ... in order.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+  __shared__ Item item;
+  __shared__ int64_t from, to, all;
+  __shared__ float weight[kMaxGrid][kJoinRows];  // maxima, then the parts' weights
+  __shared__ float sums[kMaxGrid][kJoinRows];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, c = blockIdx.x + 1;
+  if (warp == 0) {
+    const int64_t total = total_units(a), u = border(total, c, grid);
+    if (tid == 0) from = to = 0, all = total;
+    if (u < total)
+      each_item(a, u, u + 1, [&](const Item& it, int64_t at) {
+        if (tid == 0 && at < u && border(total, c - 1, grid) <= at) {
+          item = it;
+          from = at;
+          to = at + (it.hi - it.lo);
+        }
+        return false;
+      });
+  }
+  __syncthreads();
+  const int row = blockIdx.y * kJoinRows + lane;
+  if (from == to || (int)blockIdx.y * kJoinRows >= item.rows) return;
+  // parts: CTA c - 1 + k; its slot, or -1 where the CTA has no unit
+  int parts = 1;
+  while (c - 1 + parts < grid && border(all, c - 1 + parts, grid) < to) ++parts;
+  auto slot_of = [&](int k) {
+    const int x = c - 1 + k;
+    if (border(all, x, grid) == border(all, x + 1, grid)) return -1;
+    return 2 * x + (k == 0 ? 1 : 0);
+  };
+  for (int k = warp; k < parts; k += kJoinThreads / 32) {
+    const int s = slot_of(k);
+    const float2 ml = s >= 0 ? a.part_ml[(int64_t)s * kRows + row] : make_float2(-INFINITY, 0.0f);
+    weight[k][lane] = ml.x;
+    sums[k][lane] = ml.y;
+  }
+  __syncthreads();
+  float top = -INFINITY, sum = 0.0f;
+  for (int k = 0; k < parts; ++k) top = fmaxf(top, weight[k][lane]);
+  const float z = top == -INFINITY ? 0.0f : top;
+  for (int k = 0; k < parts; ++k) sum += sums[k][lane] * ex2(weight[k][lane] - z);
+  __syncthreads();
+  for (int k = warp; k < parts; k += kJoinThreads / 32) weight[k][lane] = ex2(weight[k][lane] - z);
+  __syncthreads();
+  if (row >= item.rows) return;
+  const int f = item.row0 + row, i = f / a.group, g = f % a.group;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
+  for (int x = warp; x < D / 4; x += kJoinThreads / 32) {
+    float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const int s = slot_of(k);
+      if (s < 0) continue;
+      const float4 p = a.part_o[((int64_t)s * (D / 4) + x) * kRows + row];
+      const float by = weight[k][lane];
+      o.x += p.x * by, o.y += p.y * by, o.z += p.z * by, o.w += p.w * by;
+    }
+    *reinterpret_cast<uint2*>(dst + x * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+  if (warp == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
+}
+
+size_t part_bytes(int grid, int head_dim) { return (size_t)2 * grid * kRows * (head_dim * 4 + 8); }
+
+template <int D>
+int launch(const AttnArgs& a, int grid, cudaStream_t st) {
+  constexpr int smem = Geo<D>::kCtl + (int)sizeof(Ctl);
+  static_assert(smem <= 232448, "shared memory of a block");
+  const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string("tree_attn: ") + cudaGetErrorString(e));
+  attn_kernel<D><<<grid, kThreads, smem, st>>>(a);
+  const int rc = launched("tree_attn");
+  if (rc != MK_OK || grid == 1) return rc;
+  join_kernel<D><<<dim3(grid - 1, kRows / kJoinRows), kJoinThreads, 0, st>>>(a, grid);
+  return launched("tree_attn");
+}
+
+int grid_size() {
+  const int n = mk::query_num_sms();
+  return n > kMaxGrid ? kMaxGrid : n;
 }
 
 }  // namespace
@@ -108,8 +924,8 @@ using namespace mk::ops;
 extern "C" {
 
 size_t mk_tree_attn_workspace_bytes(const mk_kv* kv) {
-  if (!kv || mk::query_num_sms() < 1) return 0;
-  return 16;
+  const int grid = kv ? grid_size() : 0;
+  return grid < 1 ? 0 : part_bytes(grid, kv->cfg.head_dim);
 }
 
 int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_io* io, void* workspace,
@@ -134,6 +950,9 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   const size_t need = mk_tree_attn_workspace_bytes(kv);
   if (need == 0) return fail(MK_ERR_CUDA, "no device");
   if (workspace_bytes < need) return fail(MK_ERR_ARG, "workspace smaller than mk_tree_attn_workspace_bytes");
+  rc = encode_pools(kv);
+  if (rc != MK_OK) return rc;
+  const int grid = grid_size();
   AttnArgs a;
   a.pools = pools_of(kv, layer);
   a.b = batch_of(tok);
@@ -141,14 +960,14 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   a.mask = io->tree_mask;
   a.q_stride = io->q_stride, a.out_stride = io->out_stride;
   a.n_q = io->n_q, a.group = io->n_q / c.n_kv, a.mask_words = io->mask_words, a.window = io->window;
-  a.scale = io->scale > 0 ? io->scale : 1.0f / std::sqrt((float)c.head_dim);
+  a.layer = layer;
+  a.scale_log2 = (float)((io->scale > 0 ? (double)io->scale : 1.0 / std::sqrt((double)c.head_dim)) * 1.4426950408889634);
+  a.part_o = static_cast<float4*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kRows * (c.head_dim / 4));
   a.status = status;
-  const dim3 grid((unsigned)tok->n_tokens, (unsigned)io->n_q);
-  if (c.head_dim == 128)
-    attn_simple<128><<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  else
-    attn_simple<64><<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched("tree_attn");
+  a.tm_k = kv->tm_k, a.tm_v = kv->tm_v;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.head_dim == 128 ? launch<128>(a, grid, st) : launch<64>(a, grid, st);
 }
 
 }  // extern "C"

@@ -364,6 +364,68 @@ def test_attn_values_outside_the_window_stay_out(kind):
             assert torch.equal(out[i], clean[i]) and torch.equal(lse[i], clean_lse[i])
 
 
+LONG = [
+    # n_q, n_kv, d, P, contexts, new tokens, mask, window: many tiles and many items for every SM
+    (32, 4, 128, 64, [2900 + 37 * b for b in range(12)], [8] * 12, "tree", 0),
+    (32, 4, 128, 16, [1500 + 91 * b for b in range(16)], [32, 17, 16, 33] * 4, "tree", 0),
+    (16, 2, 64, 64, [6000, 100, 20000, 1], [64, 1, 5, 130], "tree", 0),
+    (8, 8, 64, 32, [40 * b for b in range(200)], [1 + b % 3 for b in range(200)], None, 0),
+    (4, 4, 128, 128, [5] * 700, [2] * 700, "tree", 0),
+    (32, 4, 128, 64, [2000], [1100], None, 0),
+    (32, 4, 128, 64, [9000, 300], [700, 500], None, 4096),
+    (24, 4, 128, 64, [12000, 4097] * 6, [20, 11] * 6, "tree", 4096),
+    (16, 2, 64, 16, [0], [3000], None, 512),
+]
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,P,ctx,new,kind,window", LONG)
+def test_attn_many_units(n_q, n_kv, d, P, ctx, new, kind, window):
+    g = gen(71 + len(ctx))
+    pg = Paged(g, [a + b for a, b in zip(ctx, new)], n_kv, P, d)
+    T, B = sum(new), len(new)
+    q = (2 * torch.randn(T, n_q, d, generator=g, device=DEV)).to(BF)
+    trees = [tree_of(g, n, "tree") for n in new] if kind else None
+    kw = {}
+    if kind:
+        kw = dict(tree_mask=mask_words([m for t in trees for m in t[0]], -(-max(new) // 64)),
+                  positions=ints([c + e for c, t in zip(ctx, trees) for e in t[1]]))
+    st = new_status()
+    out, lse = run_attn(pg, q, ctx, new, window=window, status=st, **kw)
+    mk.check_status(st)
+    again = run_attn(pg, q, ctx, new, window=window, **kw)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    scale, t = 1 / math.sqrt(d), 0
+    for b in range(B):
+        n, c = new[b], ctx[b]
+        s = torch.arange(c + n, device=DEV)
+        k, v = (x[0][pg.tables[b].long()[s // P], :, s % P].double() for x in (pg.k, pg.v))
+        if kind:
+            see = torch.tensor([[True] * c + [bool(m >> j & 1) for j in range(n)] for m in trees[b][0]], device=DEV)
+            mine = torch.tensor([c + e for e in trees[b][1]], device=DEV)
+        else:
+            mine = torch.arange(c, c + n, device=DEV)
+            see = s[None] <= mine[:, None]
+        if window:
+            see = see & (mine[:, None] - torch.cat((s[:c], mine))[None] < window)
+        for h in range(n_kv):
+            G = n_q // n_kv
+            x = q[t:t + n, h * G:(h + 1) * G].double().transpose(0, 1)
+            w = (x @ k[:, h].T * scale).masked_fill(~see[None], -math.inf)
+            size = (x.abs() @ k[:, h].T.abs() * scale).amax(-1)
+            want = torch.logsumexp(w, -1)
+            p = torch.exp(w - want[..., None])
+            ref, spread = p @ v[:, h], p @ v[:, h].abs()
+            # the bounds of check_attn
+            ds = size * d * 2.0 ** -23 + 2.0 ** -20
+            far = (c + n) * 2.0 ** -24
+            tol = plain.bf16_bound(ref) + spread * (2.0 ** -8 + 2 * ds[..., None] + far) * 1.01
+            err = (out[t:t + n, h * G:(h + 1) * G].double().transpose(0, 1) - ref).abs()
+            assert (err <= tol).all(), (b, h, float((err - tol).max()))
+            le = (lse[t:t + n, h * G:(h + 1) * G].double().T - want).abs()
+            assert (le <= ds + far + want.abs() * 2.0 ** -22).all()
+        t += n
+
+
 def test_attn_extreme_scores():
     """Scores far apart (one slot takes all), equal ones, and the lowest: the running maximum must carry them."""
     g = gen(23)
