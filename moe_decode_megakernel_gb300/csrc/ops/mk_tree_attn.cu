@@ -49,6 +49,7 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   float4* part_o;    // [2 * grid][D / 4][kRows]
   float2* part_ml;   // [2 * grid][kRows]: maximum (log2 units), sum
+  struct Border* borders;  // [grid + 1]
   uint32_t* status;
   CUtensorMap tm_k, tm_v;
 };
@@ -76,6 +77,13 @@ struct Item {
   int lo, hi;                  // tiles of this part
   int masked_from, window_to;  // tiles >= the one or < the other may be masked in part
   int slot;                    // workspace slot of the part, -1: the item is whole
+};
+
+// Where a CTA's units begin: its first unit, and the whole item that holds it
+// (beginning at unit `at`; at = first where the CTA has none).
+struct Border {
+  int64_t first, at;
+  Item item;
 };
 
 struct Ctl {
@@ -136,15 +144,39 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
   return v;
 }
 
-// All units (by one warp).
-__device__ int64_t total_units(const AttnArgs& a) {
-  int64_t u = 0;
-  for (int b = threadIdx.x % 32; b < a.b.batch; b += 32) u += units_of(a, attn_seq(a, b)) * a.pools.n_kv;
-  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
-  return u;
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of numbers that are not negative
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-__device__ __forceinline__ int64_t border(int64_t total, int c, int grid) { return total * c / grid; }
+// A lane's sequence of a round of 32, and the units of one of its heads.
+struct Load {
+  Seq s;
+  int64_t per_head;
+};
+__device__ __forceinline__ Load load_of(const AttnArgs& a, int b) {
+  Load x = {{0, 0, 0}, 0};
+  if (b < a.b.batch) {
+    x.s = attn_seq(a, b);
+    x.per_head = units_of(a, x.s);
+  }
+  return x;
+}
+
+// All units (by one warp), and the lane's sequence of the first round.
+__device__ __forceinline__ int64_t total_units(const AttnArgs& a, Load& first) {
+  const int lane = threadIdx.x % 32;
+  first = load_of(a, lane);
+  int64_t u = first.per_head;
+  for (int b = lane + 32; b < a.b.batch; b += 32) u += load_of(a, b).per_head;
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
+  return u * a.pools.n_kv;
+}
+
+// The first unit of CTA c: even runs, the longer ones first.
+__device__ __forceinline__ int64_t border(int64_t total, int c, int grid) {
+  const int64_t base = divide(total, grid), rest = total - base * grid;
+  return base * c + (c < rest ? c : rest);
+}
 
 // The item of unit u at (h, m) of sequence b, whose units of this head begin
 // at unit `base`: everything but the part.
@@ -167,18 +199,16 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
 }
 
 // Calls f(item, first unit of the item) for the items that hold units [u, end),
-// in order, while it returns true.  By one warp; f runs on every lane.
+// in order, while it returns true.  By one warp, whose lanes hold the first
+// round's sequences; f runs on every lane.
 template <typename F>
-__device__ void each_item(const AttnArgs& a, int64_t u, int64_t end, F f) {
+__device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, int64_t u, int64_t end, F f) {
   const int lane = threadIdx.x % 32;
   int64_t base = 0;  // units before this round of sequences
   for (int b0 = 0; b0 < a.b.batch && base < end; b0 += 32) {
-    Seq s = {0, 0, 0};
-    int64_t per_head = 0;
-    if (b0 + lane < a.b.batch) {
-      s = attn_seq(a, b0 + lane);
-      per_head = units_of(a, s);
-    }
+    const Load x = b0 == 0 ? first : load_of(a, b0 + lane);
+    const Seq s = x.s;
+    const int64_t per_head = x.per_head;
     const int64_t incl = warp_scan(per_head * a.pools.n_kv);
     uint32_t hit = __ballot_sync(FULL, per_head > 0 && base + incl > u && base + incl - per_head * a.pools.n_kv < end);
     while (hit) {
@@ -187,7 +217,7 @@ __device__ void each_item(const AttnArgs& a, int64_t u, int64_t end, F f) {
       const Seq q = {__shfl_sync(FULL, s.t0, src), __shfl_sync(FULL, s.n, src), __shfl_sync(FULL, s.ctx, src)};
       const int64_t ph = __shfl_sync(FULL, per_head, src), begin = base + __shfl_sync(FULL, incl, src) - ph * a.pools.n_kv;
       const int M = groups_of(a, q);
-      int h = u > begin ? (int)((u - begin) / ph) : 0;
+      int h = u > begin ? (int)divide(u - begin, ph) : 0;
       for (; h < a.pools.n_kv; ++h) {
         int64_t at = begin + h * ph;
         if (at >= end) return;
@@ -208,9 +238,11 @@ __device__ void each_item(const AttnArgs& a, int64_t u, int64_t end, F f) {
 
 // ------------------------------------------------------------- waits
 
+// (No function of the roles is called: a call fixes the registers of both
+// register budgets.)
 // Waits for a phase; false when this wait, or another one of the CTA, has
 // taken too long.
-__device__ __noinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
+__device__ __forceinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
   const int64_t until = gtimer() + kWaitNs;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -359,13 +391,21 @@ __device__ bool produce(const AttnArgs& a, uint8_t* smem, Ctl& c, Ring& r, uint3
   return true;
 }
 
-// B operand with N contiguous (V as the pages hold it): 64-dim columns of
-// 128-byte rows, a K group of 8 slots every 1024 bytes, the next 64 dims a
-// half tile further.
-__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t half_bytes) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(half_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory operands of the MMAs, as their descriptors' lower words (the
+// address in 16-byte units; adding an offset's sixteenth moves the operand)
+// and a common upper word: 128-byte rows with the 128-byte swizzle, groups of
+// 8 rows every 1024 bytes.  K-major for Q and K; V as the pages hold it, N
+// contiguous, the next 64 dims a half tile further (the lower word's upper
+// half, which K-major operands ignore).
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
+
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(FULL, v, 0); }
 
 struct MmaState {
   Ring k;                        // the next K or V tile of the ring
@@ -373,16 +413,24 @@ struct MmaState {
   uint32_t q_phase = 0, v_phase = 0;  // of q_ready, of v_ok
 };
 
+// By one whole warp, so that addresses stay in uniform registers (an MMA
+// takes its operands from there: from a lone thread each costs a move per
+// operand, 80 cycles per MMA instead of the 64 that it runs); one elected lane
+// issues.
 template <int D>
-__device__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st) {
+__device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st) {
   using G = Geo<D>;
   constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kTile);
   constexpr uint32_t idesc_o = tc_idesc_bf16(kTile, D) | (1u << 16);  // B with N contiguous
-  const uint32_t base = smem_u32(smem), tmem = c.tmem;
-  for (int k = 0; k < c.n_items; ++k) {
-    const Item it = c.items[k];
-    const bool both = both_in(it);
-    const int steps = (it.hi - it.lo) << (both ? 1 : 0);
+  const uint32_t base = smem_u32(smem) >> 4, tmem = uniform(c.tmem), vlo = (G::kHalfBytes >> 4) << 16, klo = 1u << 16;
+  const bool lead = elected();
+  const int n_items = uniform(c.n_items);
+  for (int k = 0; k < n_items; ++k) {
+    const Item& it = c.items[k];
+    const bool both = uniform(both_in(it));
+    const int lo = uniform(it.lo), tiles = uniform(it.hi) - lo;
+    const int masked_from = uniform(it.masked_from) - lo, window_to = uniform(it.window_to) - lo;
+    const int steps = both ? 2 * tiles : tiles;
     // tile x of the item: K at ring position 2x, V at 2x + 1 from here on
     Ring kpos = st.k, vpos = st.k;
     vpos.advance<G::kStages>();
@@ -390,14 +438,16 @@ __device__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& s
     st.q_phase ^= 1;
     tc_fence_after();
     for (int s = -2; s < steps; ++s) {
+      const int w = s & 1;
+      const bool fresh = !both || w == 0, last = !both || w == 1;  // the first, the last use of a tile
       if (s >= 0) {  // O += P V of step s
-        const int w = s & 1;
-        const bool first = s < 2, fresh = !both || w == 0, part = fresh && in_part(it, it.lo + (both ? s >> 1 : s));
-        // This thread waits for every tile of the ring, in order (a barrier's
+        const int x = both ? s >> 1 : s;
+        const bool part = fresh && (x >= masked_from || x < window_to);
+        // This warp waits for every tile of the ring, in order (a barrier's
         // parity tells neighbouring phases apart, not those two laps apart),
         // and sends the tiles that need it to clean_v.
         if (fresh && !wait(c, &c.full[vpos.stage], vpos.phase, a.status)) return false;
-        if (part) mbar_arrive(&c.v_go);
+        if (part && lead) mbar_arrive(&c.v_go);
         if (!wait(c, &c.p_ready[w], st.p_phase[w], a.status)) return false;
         st.p_phase[w] ^= 1;
         if (part) {
@@ -405,36 +455,42 @@ __device__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& s
           st.v_phase ^= 1;
         }
         tc_fence_after();
-        const uint64_t vd = desc_v(base + G::kRing + vpos.stage * G::kTileBytes, G::kHalfBytes);
+        const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes) / 16) | vlo;
+        const uint32_t td = tmem + 256 + w * 128, ta = tmem + w * 128;
+        if (lead) {
 #pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)  // 16 slots: 8 columns of P, two 1024-byte groups of V
-          mma_bf16_ta(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * (2048 >> 4), idesc_o, !first || x > 0);
-        if (!both || w == 1) {
-          tc_commit(&c.empty[vpos.stage]);
-          vpos.advance<G::kStages>();
-          vpos.advance<G::kStages>();
+          for (int e = 0; e < kTile / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
+            mma_bf16_ta(td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, s >= 2 || e > 0);
+          if (last) tc_commit(&c.empty[vpos.stage]);
+          if (s + 2 >= steps) {  // the group's last: its arrival carries what this warp has seen, the commit the MMAs
+            mbar_arrive(&c.o_full[w]);
+            tc_commit(&c.o_full[w]);
+          }
         }
-        if (s + 2 >= steps) {  // the group's last: its arrival carries what this thread has seen, the commit the MMAs
-          mbar_arrive(&c.o_full[w]);
-          tc_commit(&c.o_full[w]);
+        if (last) {
+          vpos.advance<G::kStages>();
+          vpos.advance<G::kStages>();
         }
       }
       if (s + 2 < steps) {  // S = Q K^T of step s + 2
-        const int w = s & 1;
-        if ((!both || w == 0) && !wait(c, &c.full[kpos.stage], kpos.phase, a.status)) return false;
+        if (fresh && !wait(c, &c.full[kpos.stage], kpos.phase, a.status)) return false;
         tc_fence_after();
-        const uint32_t qa = base + G::kQ + (both ? w * G::kTileBytes : 0), ka = base + G::kRing + kpos.stage * G::kTileBytes;
+        const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
+        const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes) / 16) | klo;
+        const uint32_t ts = tmem + w * 128;
+        if (lead) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t off = x / 4 * G::kHalfBytes + x % 4 * 32;
-          tc_mma_bf16(tmem + w * 128, tc_desc_sw128(qa + off), tc_desc_sw128(ka + off), idesc_s, x > 0);
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
+            tc_mma_bf16(ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
+          }
+          if (last) tc_commit(&c.empty[kpos.stage]);
+          tc_commit(&c.s_full[w]);
         }
-        if (!both || w == 1) {
-          tc_commit(&c.empty[kpos.stage]);
+        if (last) {
           kpos.advance<G::kStages>();
           kpos.advance<G::kStages>();
         }
-        tc_commit(&c.s_full[w]);
       }
     }
     st.k = kpos;  // two positions per tile: behind the item's last V
@@ -501,6 +557,32 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two fp32 at a time (each half rounded as the scalar operation).
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  return make_float2(a, b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -510,7 +592,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // What clean_v zeroed, for the rows that see it: its products with the row's
 // probabilities, added to 32 columns of the row's output.
 template <int D>
-__device__ __noinline__ void add_odd_v(const AttnArgs& a, const Item& it, int i, int g, int pos, float m, int col, float (&o)[32]) {
+__device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int i, int g, int pos, float m, int col, float (&o)[32]) {
   const uint16_t* q = a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D;
   for (int j = it.lo; j < it.hi; ++j) {
     if (!in_part(it, j)) continue;
@@ -570,24 +652,25 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
         continue;
       }
       tc_fence_after();
-      uint32_t s[128];
-      tmem_load(t_s, s);
+      uint32_t s[2][64];
+      tmem_load(t_s, s[0]);
+      tmem_load(t_s + 64, s[1]);
       if (j >= masked_from || j < window_to) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint32_t v = seen(a, it, i, pos, j * kTile + x * 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (!((v >> e) & 1)) s[x * 32 + e] = 0xff800000u;
+            if (!((v >> e) & 1)) s[x / 2][x % 2 * 32 + e] = 0xff800000u;
         }
       }
       float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 128; e += 8) {
-        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
-        t2 = fmaxf(t2, fmaxf(__uint_as_float(s[e + 4]), __uint_as_float(s[e + 5])));
-        t3 = fmaxf(t3, fmaxf(__uint_as_float(s[e + 6]), __uint_as_float(s[e + 7])));
+      for (int e = 0; e < 64; e += 4) {
+        t0 = max3(t0, s[0][e], s[0][e + 1]);
+        t1 = max3(t1, s[0][e + 2], s[0][e + 3]);
+        t2 = max3(t2, s[1][e], s[1][e + 1]);
+        t3 = max3(t3, s[1][e + 2], s[1][e + 3]);
       }
       const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
       // The maximum in use may lag by kSlack (p <= 2^8, exact enough in bf16
@@ -609,22 +692,26 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
         m = to;
       }
       const float z = m == -INFINITY ? 0.0f : m;
-      float l0 = 0, l1 = 0, l2 = 0, l3 = 0;
+      const uint32_t zb = __float_as_uint(-z), sb = __float_as_uint(a.scale_log2);
+      const uint64_t z2 = pair(zb, zb), scale2 = pair(sb, sb);
+      uint64_t l0 = 0, l1 = 0;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
-          const uint32_t* x = s + half * 64 + e;
-          const float p0 = ex2(fmaf(__uint_as_float(x[0]), a.scale_log2, -z)), p1 = ex2(fmaf(__uint_as_float(x[1]), a.scale_log2, -z));
-          const float p2 = ex2(fmaf(__uint_as_float(x[2]), a.scale_log2, -z)), p3 = ex2(fmaf(__uint_as_float(x[3]), a.scale_log2, -z));
-          l0 += p0, l1 += p1, l2 += p2, l3 += p3;
-          p[e / 2] = pack_bf16(p0, p1);
-          p[e / 2 + 1] = pack_bf16(p2, p3);
+          const uint32_t* x = s[half] + e;
+          float2 u = halves(fma2(pair(x[0], x[1]), scale2, z2)), v = halves(fma2(pair(x[2], x[3]), scale2, z2));
+          u.x = ex2(u.x), u.y = ex2(u.y), v.x = ex2(v.x), v.y = ex2(v.y);
+          l0 = add2(l0, pair(__float_as_uint(u.x), __float_as_uint(u.y)));
+          l1 = add2(l1, pair(__float_as_uint(v.x), __float_as_uint(v.y)));
+          p[e / 2] = pack_bf16(u.x, u.y);
+          p[e / 2 + 1] = pack_bf16(v.x, v.y);
         }
         tmem_store(t_s + half * 32, p);
       }
-      l += (l0 + l1) + (l2 + l3);
+      const float2 ls = halves(add2(l0, l1));
+      l += ls.x + ls.y;
       tmem_store_wait();
       tc_fence_before();
       mbar_arrive(&c.p_ready[w]);
@@ -712,17 +799,58 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
   return true;
 }
 
+// The next items of a CTA's units [u, end), which began at `begin` (by one warp).
+__device__ __forceinline__ void plan_items(const AttnArgs& a, Ctl& c, const Load& first, int64_t begin, int64_t u, int64_t end) {
+  const bool one = threadIdx.x % 32 == 0;
+  int n = 0;
+  int64_t next = end;
+  each_item(a, first, u, end, [&](Item it, int64_t at) {
+    if (one && u == begin && n == 0) {
+      a.borders[blockIdx.x].at = at;
+      a.borders[blockIdx.x].item = it;
+    }
+    if (n == kMaxItems) {
+      next = at;
+      return false;
+    }
+    const int64_t stop = at + (it.hi - it.lo);
+    const int64_t from = at < begin ? begin : at, to = stop < end ? stop : end;
+    // a part that begins its item is the run's last, any other its first
+    if (from > at)
+      it.slot = 2 * blockIdx.x;
+    else if (to < stop)
+      it.slot = 2 * blockIdx.x + 1;
+    it.hi = it.lo + (int)(to - at);
+    it.lo += (int)(from - at);
+    if (one) {
+      c.items[n] = it;
+      c.bad_v[n] = 0;
+    }
+    ++n;
+    return true;
+  });
+  if (one) {
+    c.n_items = n;
+    c.next = next;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   using G = Geo<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl& c = *reinterpret_cast<Ctl*>(smem + G::kCtl);
   const int tid = threadIdx.x, warp = tid / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Load load;
   if (warp == 0) {
-    const int64_t total = total_units(a);
+    const int64_t total = total_units(a, load);
     if (tid == 0) {
       c.first = border(total, blockIdx.x, gridDim.x);
       c.end = border(total, blockIdx.x + 1, gridDim.x);
+      a.borders[blockIdx.x].first = c.first;
+      a.borders[blockIdx.x].at = c.first;  // until the plan says more
+      if (blockIdx.x == 0) a.borders[gridDim.x].first = total;
     }
   }
   if (tid == 0) {
@@ -752,54 +880,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (warp == 1) tmem_alloc(&c.tmem, 512);
   __syncthreads();
 
-  Ring fill;
-  CleanState check;
-  MmaState mma;
-  RowState rows;
-  uint32_t filled = 0;
+  // The softmax warps keep a row of S in registers: the other warps hand them
+  // theirs (128 x 80 + 256 x 208 of the launch's 384 x 168).
   bool ok = true;
-  while (u < end && ok) {
-    if (warp == 0) {  // the next items of this CTA's run of units
-      int n = 0;
-      int64_t next = end;
-      each_item(a, u, end, [&](Item it, int64_t at) {
-        if (n == kMaxItems) {
-          next = at;
-          return false;
-        }
-        const int64_t stop = at + (it.hi - it.lo);
-        const int64_t from = at < begin ? begin : at, to = stop < end ? stop : end;
-        // a part that begins its item is the run's last, any other its first
-        if (from > at)
-          it.slot = 2 * blockIdx.x;
-        else if (to < stop)
-          it.slot = 2 * blockIdx.x + 1;
-        it.hi = it.lo + (int)(to - at);
-        it.lo += (int)(from - at);
-        if (tid == 0) {
-          c.items[n] = it;
-          c.bad_v[n] = 0;
-        }
-        ++n;
-        return true;
-      });
-      if (tid == 0) {
-        c.n_items = n;
-        c.next = next;
-      }
+  Ring fill;
+  uint32_t filled = 0;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    CleanState check;
+    MmaState mma;
+    while (u < end && ok) {
+      if (warp == 0) plan_items(a, c, load, begin, u, end);
+      __syncthreads();
+      if (warp == 0)
+        ok = produce<D>(a, smem, c, fill, filled);
+      else if (warp == 1)
+        ok = issue_mmas<D>(a, smem, c, mma);
+      else if (warp >= 2)
+        ok = clean_v<D>(a, smem, c, check);
+      ok = __syncthreads_and(ok);
+      u = c.next;
+      __syncthreads();
     }
-    __syncthreads();
-    if (warp == 0)
-      ok = produce<D>(a, smem, c, fill, filled);
-    else if (tid == 32)
-      ok = issue_mmas<D>(a, smem, c, mma);
-    else if (warp == 2 || warp == 3)
-      ok = clean_v<D>(a, smem, c, check);
-    else if (warp >= 4)
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    RowState rows;
+    while (u < end && ok) {
+      __syncthreads();
       ok = softmax_rows<D>(a, smem, c, rows);
-    ok = __syncthreads_and(ok);
-    u = c.next;
-    __syncthreads();
+      ok = __syncthreads_and(ok);
+      u = c.next;
+      __syncthreads();
+    }
   }
   if (!ok) {
     // a wait was given up: the copies and MMAs in flight first (bounded)
@@ -812,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
       }
     }
-    if (tid == 32) {
+    if (warp == 1 && elected()) {  // the lane that issued the MMAs
       tc_commit(&c.drain);
       for (int64_t until = gtimer() + kWaitNs; !mbar_try_wait(&c.drain, 0) && gtimer() < until;) {
       }
@@ -825,45 +937,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
 // ------------------------------------------------------------- the join
 
-constexpr int kJoinRows = 32, kJoinThreads = 256, kMaxGrid = 160;
+constexpr int kJoinRows = 32, kMaxGrid = 160;
 
 // Block (c - 1, y): if the border between CTAs c - 1 and c of the first kernel
 // is the first one inside an item, joins 32 of that item's rows: the parts of
-// CTAs c - 1, c, ... in order.
+// CTAs c - 1, c, ... in order, four columns to a warp, a row to a lane.  It is
+// bound by the latency of its loads (a part's rows lie side by side: 512
+// bytes per warp and load), so every thread has one output and eight loads
+// under way.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  __shared__ Item item;
-  __shared__ int64_t from, to, all;
+__global__ void __launch_bounds__(D / 4 * 32) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+  constexpr int kWarps = D / 4;
+  __shared__ int slots[kMaxGrid];
   __shared__ float weight[kMaxGrid][kJoinRows];  // maxima, then the parts' weights
   __shared__ float sums[kMaxGrid][kJoinRows];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, c = blockIdx.x + 1;
-  if (warp == 0) {
-    const int64_t total = total_units(a), u = border(total, c, grid);
-    if (tid == 0) from = to = 0, all = total;
-    if (u < total)
-      each_item(a, u, u + 1, [&](const Item& it, int64_t at) {
-        if (tid == 0 && at < u && border(total, c - 1, grid) <= at) {
-          item = it;
-          from = at;
-          to = at + (it.hi - it.lo);
-        }
-        return false;
-      });
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Border& here = a.borders[c];
+  const int64_t first = here.first, at = here.at;
+  if (at >= first || a.borders[c - 1].first > at || (int)blockIdx.y * kJoinRows >= here.item.rows) return;
+  const int64_t to = at + (here.item.hi - here.item.lo);
+  bool part = false;
+  if (tid < grid - (c - 1)) {
+    part = a.borders[c - 1 + tid].first < to;
+    // a part that begins its item is its CTA's last, the others their CTA's first
+    slots[tid] = tid == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + tid);
   }
-  __syncthreads();
+  const int parts = __syncthreads_count(part);
   const int row = blockIdx.y * kJoinRows + lane;
-  if (from == to || (int)blockIdx.y * kJoinRows >= item.rows) return;
-  // parts: CTA c - 1 + k; its slot, or -1 where the CTA has no unit
-  int parts = 1;
-  while (c - 1 + parts < grid && border(all, c - 1 + parts, grid) < to) ++parts;
-  auto slot_of = [&](int k) {
-    const int x = c - 1 + k;
-    if (border(all, x, grid) == border(all, x + 1, grid)) return -1;
-    return 2 * x + (k == 0 ? 1 : 0);
-  };
-  for (int k = warp; k < parts; k += kJoinThreads / 32) {
-    const int s = slot_of(k);
-    const float2 ml = s >= 0 ? a.part_ml[(int64_t)s * kRows + row] : make_float2(-INFINITY, 0.0f);
+  for (int k = warp; k < parts; k += kWarps) {
+    const float2 ml = a.part_ml[(int64_t)slots[k] * kRows + row];
     weight[k][lane] = ml.x;
     sums[k][lane] = ml.y;
   }
@@ -873,28 +976,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const float z = top == -INFINITY ? 0.0f : top;
   for (int k = 0; k < parts; ++k) sum += sums[k][lane] * ex2(weight[k][lane] - z);
   __syncthreads();
-  for (int k = warp; k < parts; k += kJoinThreads / 32) weight[k][lane] = ex2(weight[k][lane] - z);
+  for (int k = warp; k < parts; k += kWarps) weight[k][lane] = ex2(weight[k][lane] - z);
   __syncthreads();
+  const Item& item = here.item;
   if (row >= item.rows) return;
   const int f = item.row0 + row, i = f / a.group, g = f % a.group;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
-  for (int x = warp; x < D / 4; x += kJoinThreads / 32) {
-    float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const int s = slot_of(k);
-      if (s < 0) continue;
-      const float4 p = a.part_o[((int64_t)s * (D / 4) + x) * kRows + row];
-      const float by = weight[k][lane];
-      o.x += p.x * by, o.y += p.y * by, o.z += p.z * by, o.w += p.w * by;
-    }
-    *reinterpret_cast<uint2*>(dst + x * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) {
+    const float4 p = a.part_o[((int64_t)slots[k] * (D / 4) + warp) * kRows + row];
+    const float by = weight[k][lane];
+    o.x += p.x * by, o.y += p.y * by, o.z += p.z * by, o.w += p.w * by;
   }
+  uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
+  *reinterpret_cast<uint2*>(dst + warp * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   if (warp == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
-size_t part_bytes(int grid, int head_dim) { return (size_t)2 * grid * kRows * (head_dim * 4 + 8); }
+size_t part_bytes(int grid, int head_dim) {
+  return (size_t)2 * grid * kRows * (head_dim * 4 + 8) + (grid + 1) * sizeof(Border);
+}
 
 template <int D>
 int launch(const AttnArgs& a, int grid, cudaStream_t st) {
@@ -905,7 +1007,18 @@ int launch(const AttnArgs& a, int grid, cudaStream_t st) {
   attn_kernel<D><<<grid, kThreads, smem, st>>>(a);
   const int rc = launched("tree_attn");
   if (rc != MK_OK || grid == 1) return rc;
-  join_kernel<D><<<dim3(grid - 1, kRows / kJoinRows), kJoinThreads, 0, st>>>(a, grid);
+  // the join may be resident (waiting) before the last parts are written
+  const int64_t rows = (int64_t)a.b.n_tokens * a.group;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows);
+  cfg.blockDim = dim3(D / 4 * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, join_kernel<D>, a, grid);
   return launched("tree_attn");
 }
 
@@ -964,6 +1077,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   a.scale_log2 = (float)((io->scale > 0 ? (double)io->scale : 1.0 / std::sqrt((double)c.head_dim)) * 1.4426950408889634);
   a.part_o = static_cast<float4*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kRows * (c.head_dim / 4));
+  a.borders = reinterpret_cast<Border*>(a.part_ml + (size_t)2 * grid * kRows);
   a.status = status;
   a.tm_k = kv->tm_k, a.tm_v = kv->tm_v;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
