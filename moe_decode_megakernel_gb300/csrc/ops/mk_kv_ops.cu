@@ -44,83 +44,108 @@ __device__ __forceinline__ float2 turn(uint64_t f, int pos) {
   return make_float2(c, s);
 }
 
-// Eight elements (a 16-byte chunk of bf16 output) of a head.
+// Eight elements (a 16-byte chunk of bf16 output) of a head, as they lie.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t elem, float (&x)[8]) {
-  if (F32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
-    const float4 a = s[0], b = s[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + elem);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Chunk {
+  uint4 u[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Chunk<F32> load8(const void* p, int64_t elem) {
+  Chunk<F32> c;
+  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + elem * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) c.u[i] = s[i];
+  return c;
+}
+__device__ __forceinline__ void values(const Chunk<true>& c, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(c.u[i].x), x[4 * i + 1] = __uint_as_float(c.u[i].y);
+    x[4 * i + 2] = __uint_as_float(c.u[i].z), x[4 * i + 3] = __uint_as_float(c.u[i].w);
+  }
+}
+__device__ __forceinline__ void values(const Chunk<false>& c, float (&x)[8]) {
+  const uint32_t w[4] = {c.u[0].x, c.u[0].y, c.u[0].z, c.u[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
-// One block per token: the token's slot and the rotation of its position
-// once, then its heads in 16-byte chunks.
+// One block per token, its heads in 16-byte chunks of output.  The first
+// chunks of every thread are on their way before the token's slot is known
+// (its sequence, then its page: two round trips to memory); the thread whose
+// sequence holds the token looks the slot up, half a head of threads turns the
+// position into sines.
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int CPH = D / 8;  // chunks per head
+  constexpr int kHeld = 3;    // chunks of a thread under way
   __shared__ float2 cs[D / 2];
   __shared__ int64_t row;  // row of head 0 in the pool, -1: not written
-  __shared__ int found;
+  __shared__ int pos, found;
   const int t = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) found = -1;
+  const int n_kv = a.pools.n_kv, heads = a.n_q + 2 * n_kv, chunks = heads * CPH;
+  Chunk<F32> held[kHeld];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      const int i = base + x * kThreads + tid, h = i / CPH, c = i % CPH;
+      if (i >= chunks) break;
+      if (h < a.n_q)
+        held[x] = load8<F32>(a.q, t * a.q_stride + h * D + c * 8);
+      else if (h < a.n_q + n_kv)
+        held[x] = load8<F32>(a.k, t * a.k_stride + (h - a.n_q) * D + c * 8);
+      else
+        held[x] = load8<F32>(a.v, t * a.v_stride + (h - a.n_q - n_kv) * D + c * 8);
+    }
+  };
+  load(0);
+  if (tid == 0) found = 0;
   __syncthreads();
-  // the sequence whose rows hold t
-  for (int b = tid; b < a.b.batch; b += kThreads)
-    if (a.b.cu[b] <= t && t < a.b.cu[b + 1]) found = b;
-  __syncthreads();
-  const int b = found;
-  if (b < 0) return;
-  const Seq s = seq_of(a.b, b, a.pools.page_shift, a.status, OP_APPEND);
-  if (s.n == 0) return;
-  const int slot = s.ctx + t - s.t0;
-  const int pos = a.b.positions ? a.b.positions[t] : slot;
-  if (tid < D / 2) cs[tid] = turn(a.freq[tid], pos);
-  if (tid == 0) {
-    const int P = 1 << a.pools.page_shift;
+  for (int b = tid; b < a.b.batch; b += kThreads) {
+    if (a.b.cu[b] > t || t >= a.b.cu[b + 1]) continue;
+    const Seq s = seq_of(a.b, b, a.pools.page_shift, a.status, OP_APPEND);
+    if (s.n == 0) continue;
+    const int slot = s.ctx + t - s.t0, P = 1 << a.pools.page_shift;
     const int page = a.b.tables[(int64_t)b * a.b.max_pages + (slot >> a.pools.page_shift)];
-    row = -1;
-    if (page < 0 || page >= a.pools.num_pages)
+    pos = a.b.positions ? a.b.positions[t] : slot;
+    row = (int64_t)page * n_kv * P + (slot & (P - 1));
+    if (page < 0 || page >= a.pools.num_pages) {
       record(a.status, dev::ERR_PAGE, OP_APPEND, b, slot, page, (uint32_t)a.pools.num_pages);
-    else
-      row = (int64_t)page * a.pools.n_kv * P + (slot & (P - 1));
+      row = -1;
+    }
+    found = 1;
   }
   __syncthreads();
-  const int n_kv = a.pools.n_kv, heads = a.n_q + 2 * n_kv;
-  for (int i = tid; i < heads * CPH; i += kThreads) {
-    const int h = i / CPH, c = i % CPH;
-    float x[8];
-    uint16_t* dst;
-    if (h < a.n_q) {
-      load8<F32>(a.q, t * a.q_stride + h * D + c * 8, x);
-      dst = a.q_out + t * a.q_out_stride + h * D + c * 8;
-    } else {
-      if (row < 0) continue;
+  if (!found) return;
+  if (tid < D / 2) cs[tid] = turn(a.freq[tid], pos);
+  __syncthreads();
+  for (int base = 0; base < chunks; base += kHeld * kThreads) {
+    if (base) load(base);
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      const int i = base + x * kThreads + tid, h = i / CPH, c = i % CPH;
+      if (i >= chunks || (h >= a.n_q && row < 0)) break;
+      float v[8];
+      values(held[x], v);
+      if (h < a.n_q + n_kv) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 w = cs[c * 4 + j];
+          const float e = v[2 * j], o = v[2 * j + 1];
+          v[2 * j] = e * w.x - o * w.y;
+          v[2 * j + 1] = e * w.y + o * w.x;
+        }
+      }
       const bool is_k = h < a.n_q + n_kv;
       const int g = h - a.n_q - (is_k ? 0 : n_kv);
-      load8<F32>(is_k ? a.k : a.v, t * (is_k ? a.k_stride : a.v_stride) + g * D + c * 8, x);
-      dst = (is_k ? a.pools.k : a.pools.v) + ((row + ((int64_t)g << a.pools.page_shift)) * D + c * 8);
+      uint16_t* dst = h < a.n_q ? a.q_out + t * a.q_out_stride + h * D + c * 8
+                                : (is_k ? a.pools.k : a.pools.v) + ((row + ((int64_t)g << a.pools.page_shift)) * D + c * 8);
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
-    if (h < a.n_q + n_kv) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 w = cs[c * 4 + j];
-        const float e = x[2 * j], o = x[2 * j + 1];
-        x[2 * j] = e * w.x - o * w.y;
-        x[2 * j + 1] = e * w.y + o * w.x;
-      }
-    }
-    uint4 u;
-    u.x = pack_bf16(x[0], x[1]), u.y = pack_bf16(x[2], x[3]), u.z = pack_bf16(x[4], x[5]), u.w = pack_bf16(x[6], x[7]);
-    *reinterpret_cast<uint4*>(dst) = u;
   }
 }
 
@@ -149,6 +174,10 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
   const int32_t* table = a.tables + (int64_t)b * a.max_pages;
   const int64_t slots = (int64_t)a.max_pages << a.pools.page_shift;
   bool bad = ctx < 0 || m < 0 || m > a.max_path;
+  const int P1 = (1 << a.pools.page_shift) - 1;
+  auto row_of = [&](int page, int slot) {
+    return (((int64_t)page * a.pools.n_kv) << a.pools.page_shift) + (slot & P1);
+  };
   if (!bad)
     for (int k = tid; k < m; k += kThreads) {
       const int s = path[k];
@@ -160,6 +189,10 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
         if (page < 0 || page >= a.pools.num_pages || dst < 0 || dst >= a.pools.num_pages) {
           bad = true;
           record(a.status, dev::ERR_PAGE, OP_COMMIT, b, k, page, (uint32_t)a.pools.num_pages);
+        }
+        if (k < kRound) {
+          from[k] = s == k ? -1 : row_of(page, ctx + s);
+          to[k] = row_of(dst, ctx + k);
         }
       }
     }
@@ -177,16 +210,17 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
   uint16_t* pool = rest < per_layer / 2 ? a.pools.k : a.pools.v;
   uint4* base = reinterpret_cast<uint4*>(pool + (mine ? layer * a.pools.layer_elems : 0));
   const int64_t head = (int64_t)h << a.pools.page_shift;
-  const int P1 = (1 << a.pools.page_shift) - 1;
   for (int k0 = 0; k0 < m; k0 += kRound) {
-    __syncthreads();
-    if (tid < kRound) {
-      const int k = k0 + tid;
-      from[tid] = to[tid] = -1;
-      if (k < m && path[k] != k) {
-        const int s = ctx + path[k], d = ctx + k;
-        from[tid] = (((int64_t)table[s >> a.pools.page_shift] * a.pools.n_kv) << a.pools.page_shift) + (s & P1);
-        to[tid] = (((int64_t)table[d >> a.pools.page_shift] * a.pools.n_kv) << a.pools.page_shift) + (d & P1);
+    if (k0) {
+      __syncthreads();
+      if (tid < kRound) {
+        const int k = k0 + tid;
+        from[tid] = -1;
+        if (k < m && path[k] != k) {
+          const int s = ctx + path[k], d = ctx + k;
+          from[tid] = row_of(table[s >> a.pools.page_shift], s);
+          to[tid] = row_of(table[d >> a.pools.page_shift], d);
+        }
       }
     }
     __syncthreads();
@@ -195,10 +229,10 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
       uint4 x[kHeld];
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
-        if (from[k + j] >= 0) x[j] = base[(from[k + j] + head) * a.row_chunks + c];
+        if (k0 + k + j < m && from[k + j] >= 0) x[j] = base[(from[k + j] + head) * a.row_chunks + c];
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
-        if (from[k + j] >= 0) base[(to[k + j] + head) * a.row_chunks + c] = x[j];
+        if (k0 + k + j < m && from[k + j] >= 0) base[(to[k + j] + head) * a.row_chunks + c] = x[j];
     }
   }
 }
@@ -283,7 +317,15 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     uint4* pool = reinterpret_cast<uint4*>((w / a.pools.n_kv % 2 ? a.pools.v : a.pools.k) + layer * a.pools.layer_elems);
     const uint4* from = pool + (((int64_t)src[e] * a.pools.n_kv + h) << a.pools.page_shift) * a.row_chunks;
     uint4* to = pool + (((int64_t)dst[e] * a.pools.n_kv + h) << a.pools.page_shift) * a.row_chunks;
-    for (int i = tid; i < run; i += kThreads) to[i] = from[i];
+    for (int i = tid; i < run; i += 4 * kThreads) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j * kThreads < run) x[j] = from[i + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j * kThreads < run) to[i + j * kThreads] = x[j];
+    }
   }
 }
 

@@ -110,8 +110,8 @@ __device__ __forceinline__ Seq attn_seq(const AttnArgs& a, int b) {
 
 // Tiles [lo, hi) of query group m of a sequence.
 __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Seq& s, int m, int& lo, int& hi) {
-  const int64_t all = (int64_t)s.n * a.group, r0 = (int64_t)m * kRows, r1 = r0 + kRows < all ? r0 + kRows : all;
-  const int i0 = (int)(r0 / a.group), i1 = (int)((r1 - 1) / a.group);
+  const int all = s.n * a.group, r0 = m * kRows, r1 = all - r0 < kRows ? all : r0 + kRows;  // below 2^31
+  const int i0 = a.mask ? 0 : (uint32_t)r0 / (uint32_t)a.group, i1 = a.mask ? 0 : (uint32_t)(r1 - 1) / (uint32_t)a.group;
   const int end = s.ctx + (a.mask ? s.n : i1 + 1);
   hi = (end + kTile - 1) / kTile;
   lo = 0;
@@ -122,7 +122,7 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Seq& s, int m,
 }
 
 __device__ __forceinline__ int groups_of(const AttnArgs& a, const Seq& s) {
-  return (int)(((int64_t)s.n * a.group + kRows - 1) / kRows);
+  return (s.n * a.group - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
 
 // Units of one K/V head of a sequence.
@@ -183,11 +183,10 @@ __device__ __forceinline__ int64_t border(int64_t total, int c, int grid) {
 __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b, int h, int m) {
   Item it;
   it.b = b, it.h = h, it.t0 = s.t0, it.n = s.n, it.ctx = s.ctx;
-  const int64_t all = (int64_t)s.n * a.group;
   it.row0 = m * kRows;
-  it.rows = all - it.row0 < kRows ? (int)(all - it.row0) : kRows;
+  it.rows = s.n * a.group - it.row0 < kRows ? s.n * a.group - it.row0 : kRows;
   tiles_of(a, s, m, it.lo, it.hi);
-  const int i0 = it.row0 / a.group, i1 = (it.row0 + it.rows - 1) / a.group;
+  const int i0 = (uint32_t)it.row0 / (uint32_t)a.group, i1 = (uint32_t)(it.row0 + it.rows - 1) / (uint32_t)a.group;
   it.masked_from = (s.ctx + (a.mask ? 0 : i0 + 1)) / kTile;
   it.window_to = 0;
   if (a.window) {
@@ -937,17 +936,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
 // ------------------------------------------------------------- the join
 
-constexpr int kJoinRows = 32, kMaxGrid = 160;
+constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinCols = kJoinThreads / 32 * 4, kMaxGrid = 160;
 
-// Block (c - 1, y): if the border between CTAs c - 1 and c of the first kernel
-// is the first one inside an item, joins 32 of that item's rows: the parts of
-// CTAs c - 1, c, ... in order, four columns to a warp, a row to a lane.  It is
-// bound by the latency of its loads (a part's rows lie side by side: 512
-// bytes per warp and load), so every thread has one output and eight loads
-// under way.
+// Block (c - 1, y, z): if the border between CTAs c - 1 and c of the first
+// kernel is the first one inside an item, joins 32 rows and 32 columns of that
+// item: the parts of CTAs c - 1, c, ... in order, four columns to a warp, a
+// row to a lane.  It is bound by the latency of its loads (a part's rows lie
+// side by side: 512 bytes per warp and load), so a thread has one output of
+// four columns and eight loads under way, and few parts share an SM.
 template <int D>
-__global__ void __launch_bounds__(D / 4 * 32) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  constexpr int kWarps = D / 4;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+  constexpr int kWarps = kJoinThreads / 32;
   __shared__ int slots[kMaxGrid];
   __shared__ float weight[kMaxGrid][kJoinRows];  // maxima, then the parts' weights
   __shared__ float sums[kMaxGrid][kJoinRows];
@@ -982,16 +981,17 @@ __global__ void __launch_bounds__(D / 4 * 32) join_kernel(const __grid_constant_
   if (row >= item.rows) return;
   const int f = item.row0 + row, i = f / a.group, g = f % a.group;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int col = blockIdx.z * kWarps + warp;  // in fours
   float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll 8
   for (int k = 0; k < parts; ++k) {
-    const float4 p = a.part_o[((int64_t)slots[k] * (D / 4) + warp) * kRows + row];
+    const float4 p = a.part_o[((int64_t)slots[k] * (D / 4) + col) * kRows + row];
     const float by = weight[k][lane];
     o.x += p.x * by, o.y += p.y * by, o.z += p.z * by, o.w += p.w * by;
   }
   uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
-  *reinterpret_cast<uint2*>(dst + warp * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (warp == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
+  *reinterpret_cast<uint2*>(dst + col * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (col == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
 size_t part_bytes(int grid, int head_dim) {
@@ -1010,8 +1010,8 @@ int launch(const AttnArgs& a, int grid, cudaStream_t st) {
   // the join may be resident (waiting) before the last parts are written
   const int64_t rows = (int64_t)a.b.n_tokens * a.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows);
-  cfg.blockDim = dim3(D / 4 * 32);
+  cfg.gridDim = dim3(grid - 1, rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows, D / kJoinCols);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1048,6 +1048,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   const mk_kv_config& c = kv->cfg;
   if (!io || !io->q || !io->out) return fail(MK_ERR_ARG, "null q or out");
   if (io->n_q < c.n_kv || io->n_q % c.n_kv != 0 || io->n_q > (1 << 16)) return fail(MK_ERR_ARG, "n_q must be a multiple of n_kv");
+  if ((int64_t)tok->n_tokens * (io->n_q / c.n_kv) > INT32_MAX) return fail(MK_ERR_ARG, "more than 2^31 - 1 query rows per K/V head");
   const int64_t row = (int64_t)io->n_q * c.head_dim;
   if (misaligned(io->q) || misaligned(io->out) || io->q_stride < row || io->out_stride < row || io->q_stride % 8 ||
       io->out_stride % 8)

@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import MK_ERR_ARG, MkError, _check, lib
+from . import MK_ERR_ARG, MkError, _check, last_error, lib
 
 MK_BF16, MK_F32 = 0, 1
 
@@ -99,28 +99,24 @@ def _rows(t, name: str, dtype, shape, device):
     return t.data_ptr(), (s[0] if shape[0] > 1 else shape[1] * shape[2])
 
 
-class _On:
-    """The tensors' device made current for a call, if it is not."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None
-        if device.type != "cuda":
-            _bad(f"tensors on {device}: a CUDA device is wanted")
-        if stream is not None and stream.device != device:
-            _bad(f"a stream of {stream.device} for tensors on {device}")
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.stream = (stream or torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.guard.__exit__(*exc)
+def _call(fn, device, stream, *args) -> None:
+    """fn(*args, raw stream) with the tensors' device current."""
+    import torch
+    if device.type != "cuda":
+        _bad(f"tensors on {device}: a CUDA device is wanted")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        _bad(f"a stream of {stream.device} for tensors on {device}")
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc:
+        raise MkError(rc, last_error())
 
 
 class KvCache:
@@ -185,13 +181,13 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
         io.q_out, io.q_out_stride = _rows(q_out, "q_out", torch.bfloat16, (T, io.n_q, d), dev)
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     st = _status(status, dev)
-    with _On(dev, stream) as s:
-        _check(_lib().mk_kv_append(cache.handle, layer, tok, io, st, s))
+    _call(_lib().mk_kv_append, dev, stream, cache.handle, layer, tok, io, st)
 
 
 def tree_attn_workspace_bytes(cache: KvCache) -> int:
     """mk_tree_attn_workspace_bytes on the cache's device."""
-    with _On(cache.device, None):
+    import torch
+    with torch.cuda.device(cache.device):
         return int(_lib().mk_tree_attn_workspace_bytes(cache.handle))
 
 
@@ -218,8 +214,7 @@ def tree_attn(cache: KvCache, layer: int, q, out, cu_seqlens, cache_lens, block_
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     ws = _take(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     st = _status(status, dev)
-    with _On(dev, stream) as s:
-        _check(_lib().mk_tree_attn(cache.handle, layer, tok, io, ws, workspace.numel(), st, s))
+    _call(_lib().mk_tree_attn, dev, stream, cache.handle, layer, tok, io, ws, workspace.numel(), st)
 
 
 def kv_commit(cache: KvCache, cache_lens, path, path_lens, block_tables, new_lens=None, status=None,
@@ -232,8 +227,7 @@ def kv_commit(cache: KvCache, cache_lens, path, path_lens, block_tables, new_len
             _take(path_lens, "path_lens", i32, (B,), dev), width,
             _take(block_tables, "block_tables", i32, (B, pages), dev), pages,
             _take(new_lens, "new_lens", i32, (B,), dev), _status(status, dev))
-    with _On(dev, stream) as s:
-        _check(_lib().mk_kv_commit(cache.handle, B, *args, s))
+    _call(_lib().mk_kv_commit, dev, stream, cache.handle, B, *args)
 
 
 def beam_select_workspace_bytes(requests: int, beams: int, vocab: int, n_out: int) -> int:
@@ -259,8 +253,7 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, 
             _take(out_scores, "out_scores", f32, (R, n), dev), _take(out_parents, "out_parents", i32, (R, n), dev),
             _take(out_tokens, "out_tokens", i32, (R, n), dev),
             _take(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel())
-    with _On(dev, stream) as s:
-        _check(_lib().mk_beam_select(logits.data_ptr(), *args, s))
+    _call(_lib().mk_beam_select, dev, stream, logits.data_ptr(), *args)
 
 
 def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=None, stream=None) -> None:
@@ -274,13 +267,11 @@ def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=No
     args = (R, W, _take(lens, "lens", i32, (R,), dev), _take(parents, "parents", i32, (R, W), dev),
             _take(tables_in, "tables_in", i32, (R * W, pages), dev),
             _take(tables_out, "tables_out", i32, (R * W, pages), dev), pages, _status(status, dev))
-    with _On(dev, stream) as s:
-        _check(_lib().mk_beam_reorder(cache.handle, *args, s))
+    _call(_lib().mk_beam_reorder, dev, stream, cache.handle, *args)
 
 
 def check_status(status, stream=None) -> None:
     """mk_check_status: waits for the stream; raises MkError if a call that
     was given `status` found a value out of range or gave up a wait."""
     st = _status(status, status.device)
-    with _On(status.device, stream) as s:
-        _check(_lib().mk_check_status(st, s))
+    _call(_lib().mk_check_status, status.device, stream, st)
