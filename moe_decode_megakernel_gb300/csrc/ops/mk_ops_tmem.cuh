@@ -1,5 +1,4 @@
-// mk_ops_tmem.cuh -- tensor-memory loads and stores of many columns, and the
-// MMA that takes its first operand from tensor memory.
+// mk_ops_tmem.cuh -- tensor-memory loads and stores of many columns.
 //
 // A thread's registers hold consecutive 32-bit columns of its TMEM lane (the
 // warp's quarter of the lanes).  Each load carries its wait in the same
@@ -59,16 +58,6 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
 }
 // Waits until this thread's tensor-memory stores are done.
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem]: BF16 operands, fp32 accumulator; a lane of A
-// holds a row, two elements of K per column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 }  // namespace ops
 }  // namespace mk

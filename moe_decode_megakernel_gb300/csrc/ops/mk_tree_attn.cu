@@ -24,8 +24,9 @@
 //   warps 4-11  two groups of 128 threads, a thread per query row: S from
 //               tensor memory, the running maximum and sum, P back as bf16
 // The two groups take the two halves of 256 query rows, or, where an item has
-// at most 128 rows, its even and odd tiles: one group's exponentials run under
-// the other's MMAs.
+// at most 128 rows, the two halves of every tile's slots.  S comes in pieces of
+// 64 slots, two buffers a group: while a group works on one piece the MMAs
+// make its next one and the other group's.
 #include <cmath>
 
 #include "mk_ops_common.cuh"
@@ -55,9 +56,10 @@ struct AttnArgs {
 };
 
 constexpr int kTile = 128;               // slots of a K/V tile, rows of an MMA
+constexpr int kPiece = kTile / 2;        // slots of a piece of S
 constexpr int kRows = 2 * kTile;         // query rows of an item
 constexpr int kThreads = 384;
-constexpr int kMaxItems = 16;            // items planned at a time
+constexpr int kMaxItems = 8;             // items planned at a time
 constexpr float kSlack = 8.0f;           // log2: how far the maximum in use may lag
 constexpr int64_t kWaitNs = 2000000000;  // a wait that takes longer is given up
 
@@ -87,14 +89,14 @@ struct Border {
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8], s_full[2], p_ready[2], o_full[2], v_go, v_ok, q_ready, rows_done, drain;
+  uint64_t full[8], empty[8], s_full[2][2], p_ready[2][2], o_full[2], v_go, v_ok, q_ready, rows_done, drain;
   uint32_t tmem, abort;
   int n_items, ok;
   int64_t first, end;  // this CTA's units
   int64_t next;
   int bad_v[kMaxItems];  // an infinity or NaN was zeroed in one of the item's tiles
   Item items[kMaxItems];
-  float2 ml[kTile];      // the second group's maxima and sums
+  float2 ml[2][kTile];   // the groups' maxima and sums
 };
 
 // ------------------------------------------------------------- the plan
@@ -399,30 +401,74 @@ __device__ bool produce(const AttnArgs& a, uint8_t* smem, Ctl& c, Ring& r, uint3
 constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
 
-__device__ __forceinline__ bool elected() {
+__device__ __forceinline__ uint32_t elected() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
+  return r;
+}
+// The lane for which `on` is not zero issues.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+// A from tensor memory: a lane holds a row, two elements of K per column.
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}" ::"r"(bar),
+      "r"(on)
+      : "memory");
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(FULL, v, 0); }
 
+// TMEM columns: four pieces of S (P takes the first half of its piece), then
+// the two groups' outputs.
+__device__ __forceinline__ uint32_t s_cols(int w, int buf) { return (w * 2 + buf) * kPiece; }
+__device__ __forceinline__ uint32_t o_cols(int w) { return 4 * kPiece + w * 128; }
+
 struct MmaState {
   Ring k;                        // the next K or V tile of the ring
-  uint32_t p_phase[2] = {0, 0};  // of p_ready
+  uint32_t p_phase = 0;          // of p_ready, a bit per group and buffer
   uint32_t q_phase = 0, v_phase = 0;  // of q_ready, of v_ok
 };
 
-// By one whole warp, so that addresses stay in uniform registers (an MMA
-// takes its operands from there: from a lone thread each costs a move per
-// operand, 80 cycles per MMA instead of the 64 that it runs); one elected lane
-// issues.
+// Step t of group w is a piece of 64 slots: with 256 rows tile t / 2, half
+// t % 2 for both groups, with 128 rows half w of tile t.  S of step t + 2 is
+// made right after O takes step t, whose buffer it reuses; MMAs run in the
+// order of their issue.  s_full[w][t % 2] then says that step t + 2 of S is
+// there and P V of step t is done.
+//
+// By one whole warp without branches on the lane: an MMA takes its operands
+// from uniform registers, and only code that all lanes run together keeps its
+// addresses there (issued by a lone thread an MMA costs 80 cycles, behind a
+// branch of one lane 45, where it runs 32 or 64).  One elected lane issues.
 template <int D>
 __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st) {
   using G = Geo<D>;
-  constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kTile);
+  constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kPiece);
   constexpr uint32_t idesc_o = tc_idesc_bf16(kTile, D) | (1u << 16);  // B with N contiguous
   const uint32_t base = smem_u32(smem) >> 4, tmem = uniform(c.tmem), vlo = (G::kHalfBytes >> 4) << 16, klo = 1u << 16;
-  const bool lead = elected();
+  const uint32_t empty = smem_u32(c.empty), s_full = smem_u32(c.s_full);
+  const uint32_t lead = elected();
+  // The warp's lanes leave every wait together: one that fell behind could
+  // miss a phase of a barrier and wait for its parity for good.
+  auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL, wait(c, bar, parity, a.status)) != 0; };
   const int n_items = uniform(c.n_items);
   for (int k = 0; k < n_items; ++k) {
     const Item& it = c.items[k];
@@ -433,65 +479,64 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
     // tile x of the item: K at ring position 2x, V at 2x + 1 from here on
     Ring kpos = st.k, vpos = st.k;
     vpos.advance<G::kStages>();
-    if (!wait(c, &c.q_ready, st.q_phase, a.status)) return false;
+    if (!ready(&c.q_ready, st.q_phase)) return false;
     st.q_phase ^= 1;
     tc_fence_after();
-    for (int s = -2; s < steps; ++s) {
-      const int w = s & 1;
-      const bool fresh = !both || w == 0, last = !both || w == 1;  // the first, the last use of a tile
-      if (s >= 0) {  // O += P V of step s
-        const int x = both ? s >> 1 : s;
-        const bool part = fresh && (x >= masked_from || x < window_to);
-        // This warp waits for every tile of the ring, in order (a barrier's
-        // parity tells neighbouring phases apart, not those two laps apart),
-        // and sends the tiles that need it to clean_v.
-        if (fresh && !wait(c, &c.full[vpos.stage], vpos.phase, a.status)) return false;
-        if (part && lead) mbar_arrive(&c.v_go);
-        if (!wait(c, &c.p_ready[w], st.p_phase[w], a.status)) return false;
-        st.p_phase[w] ^= 1;
-        if (part) {
-          if (!wait(c, &c.v_ok, st.v_phase, a.status)) return false;
-          st.v_phase ^= 1;
-        }
-        tc_fence_after();
-        const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes) / 16) | vlo;
-        const uint32_t td = tmem + 256 + w * 128, ta = tmem + w * 128;
-        if (lead) {
+    for (int t = -2; t < steps; ++t) {
+      const int buf = t & 1;
 #pragma unroll
-          for (int e = 0; e < kTile / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
-            mma_bf16_ta(td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, s >= 2 || e > 0);
-          if (last) tc_commit(&c.empty[vpos.stage]);
-          if (s + 2 >= steps) {  // the group's last: its arrival carries what this warp has seen, the commit the MMAs
-            mbar_arrive(&c.o_full[w]);
-            tc_commit(&c.o_full[w]);
+      for (int w = 0; w < 2; ++w) {
+        const int half = both ? buf : w;                                          // of step t and of step t + 2
+        const bool fresh = w == 0 && (!both || buf == 0), last = w == 1 && (!both || buf == 1);  // uses of a tile
+        if (t >= 0) {  // O += P V of step t
+          const int x = both ? t >> 1 : t;
+          const bool part = fresh && (x >= masked_from || x < window_to);
+          // This warp waits for every tile of the ring, in order (a barrier's
+          // parity tells neighbouring phases apart, not those two laps apart),
+          // and sends the tiles that need it to clean_v.
+          if (fresh && !ready(&c.full[vpos.stage], vpos.phase)) return false;
+          if (part) arrive_if(lead, smem_u32(&c.v_go));
+          if (!ready(&c.p_ready[w][buf], st.p_phase >> (w * 2 + buf) & 1)) return false;
+          st.p_phase ^= 1u << (w * 2 + buf);
+          if (part) {
+            if (!ready(&c.v_ok, st.v_phase)) return false;
+            st.v_phase ^= 1;
+          }
+          tc_fence_after();
+          const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | vlo;
+          const uint32_t td = tmem + o_cols(w), ta = tmem + s_cols(w, buf);
+#pragma unroll
+          for (int e = 0; e < kPiece / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
+            mma_ts_if(lead, td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, t > 0 || e > 0);
+          if (last) {
+            commit_if(lead, empty + vpos.stage * 8);
+            vpos.advance<G::kStages>();
+            vpos.advance<G::kStages>();
           }
         }
-        if (last) {
-          vpos.advance<G::kStages>();
-          vpos.advance<G::kStages>();
-        }
-      }
-      if (s + 2 < steps) {  // S = Q K^T of step s + 2
-        if (fresh && !wait(c, &c.full[kpos.stage], kpos.phase, a.status)) return false;
-        tc_fence_after();
-        const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
-        const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes) / 16) | klo;
-        const uint32_t ts = tmem + w * 128;
-        if (lead) {
+        if (t + 2 < steps) {  // S = Q K^T of step t + 2
+          if (fresh && !ready(&c.full[kpos.stage], kpos.phase)) return false;
+          tc_fence_after();
+          const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
+          const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | klo;
+          const uint32_t ts = tmem + s_cols(w, buf);
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
-            tc_mma_bf16(ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
+            mma_ss_if(lead, ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
           }
-          if (last) tc_commit(&c.empty[kpos.stage]);
-          tc_commit(&c.s_full[w]);
+          if (last) {
+            commit_if(lead, empty + kpos.stage * 8);
+            kpos.advance<G::kStages>();
+            kpos.advance<G::kStages>();
+          }
         }
-        if (last) {
-          kpos.advance<G::kStages>();
-          kpos.advance<G::kStages>();
-        }
+        if (t >= 0 || t + 2 < steps) commit_if(lead, s_full + (w * 2 + buf) * 8);
       }
     }
+    // what this warp has seen (clean_v's word on the item), to the groups
+    arrive_if(lead, smem_u32(&c.o_full[0]));
+    arrive_if(lead, smem_u32(&c.o_full[1]));
     st.k = kpos;  // two positions per tile: behind the item's last V
   }
   return true;
@@ -548,7 +593,8 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
 }
 
 struct RowState {
-  uint32_t s_phase = 0, o_phase = 0, done_phase = 0;
+  uint32_t s_phase = 0;  // of s_full, a bit per buffer
+  uint32_t o_phase = 0, done_phase = 0;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -611,65 +657,89 @@ __device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int
   }
 }
 
+// Q of an item: 16-byte chunks of its rows, first into registers, then into the
+// MMA's K-major layout.
 template <int D>
-__device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState& st) {
+struct QTile {
+  static constexpr int kChunks = kRows * (D / 8) / 256;  // of a thread
+  uint4 u[kChunks];
+};
+template <int D>
+__device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, QTile<D>& q) {
+  const int tid = threadIdx.x - 128, ch = tid % (D / 8), n = both_in(it) ? QTile<D>::kChunks : QTile<D>::kChunks / 2;
+#pragma unroll
+  for (int x = 0; x < QTile<D>::kChunks; ++x) {
+    const int row = tid / (D / 8) + x * (256 / (D / 8));
+    q.u[x] = make_uint4(0, 0, 0, 0);
+    if (x < n && row < it.rows) {
+      const uint32_t f = it.row0 + row, i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
+      q.u[x] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D) + ch);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_q(uint8_t* smem, bool both, const QTile<D>& q) {
+  using G = Geo<D>;
+  const int tid = threadIdx.x - 128, ch = tid % (D / 8);
+#pragma unroll
+  for (int x = 0; x < QTile<D>::kChunks; ++x) {
+    const int row = tid / (D / 8) + x * (256 / (D / 8)), rr = row % kTile;
+    if (x < (both ? QTile<D>::kChunks : QTile<D>::kChunks / 2))
+      *reinterpret_cast<uint4*>(smem + G::kQ + row / kTile * G::kTileBytes + ch / 8 * G::kHalfBytes + rr * 128 + ((ch % 8) ^ (rr & 7)) * 16) = q.u[x];
+  }
+}
+
+template <int D>
+__device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState& st) {
   using G = Geo<D>;
   const int tid = threadIdx.x - 128, w = tid / 128, r = tid % 128;
   const uint32_t lane_base = c.tmem + ((uint32_t)(r / 32 * 32) << 16);
-  const uint32_t t_s = lane_base + w * 128, t_o = lane_base + 256 + w * 128;
+  const uint32_t t_o = lane_base + o_cols(w);
+  QTile<D> q;
+  if (c.n_items > 0) load_q<D>(a, c.items[0], q);
   for (int k = 0; k < c.n_items; ++k) {
     const Item& it = c.items[k];
     const bool both = both_in(it);
-    // Q: 16-byte chunks of the item's rows, into the MMA's K-major layout
-    const int q_rows = both ? kRows : kTile;
-    for (int x = tid; x < q_rows * (D / 8); x += 256) {
-      const int row = x / (D / 8), ch = x % (D / 8);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (row < it.rows) {
-        const int f = it.row0 + row, i = f / a.group, g = f % a.group;
-        u = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D) + ch);
-      }
-      const int rr = row % kTile;
-      uint8_t* dst = smem + G::kQ + row / kTile * G::kTileBytes + ch / 8 * G::kHalfBytes + rr * 128 + ((ch % 8) ^ (rr & 7)) * 16;
-      *reinterpret_cast<uint4*>(dst) = u;
-    }
+    store_q<D>(smem, both, q);
     fence_proxy_async_smem();
     mbar_arrive(&c.q_ready);
 
     const int local = both ? w * kTile + r : r;  // row of the item
     const bool mine = local < it.rows;
     const bool warp_mine = (both ? w * kTile : 0) + r / 32 * 32 < it.rows;
-    const int f = it.row0 + (mine ? local : 0), i = f / a.group, g = f % a.group;
+    const uint32_t f = it.row0 + (mine ? local : 0);
+    const int i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
     const int pos = a.window ? position_of(a, it, i) : 0;
     float m = -INFINITY, l = 0.0f;
-    const int j0 = it.lo + (both ? 0 : w), dj = both ? 1 : 2, hi = it.hi, masked_from = it.masked_from, window_to = it.window_to;
-    for (int j = j0; j < hi; j += dj) {
-      if (!__all_sync(FULL, wait(c, &c.s_full[w], st.s_phase, a.status))) return false;
-      st.s_phase ^= 1;
+    const int lo = it.lo, steps = both ? 2 * (it.hi - lo) : it.hi - lo, masked_from = it.masked_from, window_to = it.window_to;
+    for (int t = 0; t < steps; ++t) {
+      const int buf = t & 1, j = lo + (both ? t >> 1 : t);
+      if (!__all_sync(FULL, wait(c, &c.s_full[w][buf], st.s_phase >> buf & 1, a.status))) return false;
+      st.s_phase ^= 1u << buf;
       if (!warp_mine) {  // no row of this warp: P's lanes are never used
-        mbar_arrive(&c.p_ready[w]);
+        mbar_arrive(&c.p_ready[w][buf]);
         continue;
       }
       tc_fence_after();
-      uint32_t s[2][64];
-      tmem_load(t_s, s[0]);
-      tmem_load(t_s + 64, s[1]);
+      const uint32_t t_s = lane_base + s_cols(w, buf);
+      uint32_t s[kPiece];
+      tmem_load(t_s, s);
       if (j >= masked_from || j < window_to) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t v = seen(a, it, i, pos, j * kTile + x * 32);
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t v = seen(a, it, i, pos, j * kTile + (both ? buf : w) * kPiece + x * 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (!((v >> e) & 1)) s[x / 2][x % 2 * 32 + e] = 0xff800000u;
+            if (!((v >> e) & 1)) s[x * 32 + e] = 0xff800000u;
         }
       }
       float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-        t0 = max3(t0, s[0][e], s[0][e + 1]);
-        t1 = max3(t1, s[0][e + 2], s[0][e + 3]);
-        t2 = max3(t2, s[1][e], s[1][e + 1]);
-        t3 = max3(t3, s[1][e + 2], s[1][e + 3]);
+      for (int e = 0; e < kPiece; e += 8) {
+        t0 = max3(t0, s[e], s[e + 1]);
+        t1 = max3(t1, s[e + 2], s[e + 3]);
+        t2 = max3(t2, s[e + 4], s[e + 5]);
+        t3 = max3(t3, s[e + 6], s[e + 7]);
       }
       const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
       // The maximum in use may lag by kSlack (p <= 2^8, exact enough in bf16
@@ -677,8 +747,11 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
       const bool up = top > m + kSlack;
       if (__any_sync(FULL, up)) {
         const float to = up ? top : m, by = up ? ex2(m - to) : 1.0f;
-        if (j != j0) {  // S of this step is ready, so P V of the one before is done
-#pragma unroll
+        if (t > 0) {
+          // P V of the step before is done once the next one's barrier says so
+          if (!__all_sync(FULL, wait(c, &c.s_full[w][buf ^ 1], st.s_phase >> (buf ^ 1) & 1, a.status))) return false;
+          tc_fence_after();
+#pragma unroll 1
           for (int x = 0; x < D; x += 32) {
             uint32_t o[32];
             tmem_load(t_o + x, o);
@@ -694,73 +767,74 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
       const uint32_t zb = __float_as_uint(-z), sb = __float_as_uint(a.scale_log2);
       const uint64_t z2 = pair(zb, zb), scale2 = pair(sb, sb);
       uint64_t l0 = 0, l1 = 0;
+      uint32_t p[kPiece / 2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const uint32_t* x = s[half] + e;
-          float2 u = halves(fma2(pair(x[0], x[1]), scale2, z2)), v = halves(fma2(pair(x[2], x[3]), scale2, z2));
-          u.x = ex2(u.x), u.y = ex2(u.y), v.x = ex2(v.x), v.y = ex2(v.y);
-          l0 = add2(l0, pair(__float_as_uint(u.x), __float_as_uint(u.y)));
-          l1 = add2(l1, pair(__float_as_uint(v.x), __float_as_uint(v.y)));
-          p[e / 2] = pack_bf16(u.x, u.y);
-          p[e / 2 + 1] = pack_bf16(v.x, v.y);
-        }
-        tmem_store(t_s + half * 32, p);
+      for (int e = 0; e < kPiece; e += 4) {
+        float2 u = halves(fma2(pair(s[e], s[e + 1]), scale2, z2)), v = halves(fma2(pair(s[e + 2], s[e + 3]), scale2, z2));
+        u.x = ex2(u.x), u.y = ex2(u.y), v.x = ex2(v.x), v.y = ex2(v.y);
+        l0 = add2(l0, pair(__float_as_uint(u.x), __float_as_uint(u.y)));
+        l1 = add2(l1, pair(__float_as_uint(v.x), __float_as_uint(v.y)));
+        p[e / 2] = pack_bf16(u.x, u.y);
+        p[e / 2 + 1] = pack_bf16(v.x, v.y);
       }
+      tmem_store(t_s, p);
       const float2 ls = halves(add2(l0, l1));
       l += ls.x + ls.y;
       tmem_store_wait();
       tc_fence_before();
-      mbar_arrive(&c.p_ready[w]);
+      mbar_arrive(&c.p_ready[w][buf]);
     }
 
-    // the output
-    const bool any = j0 < hi;
-    if (any) {
-      if (!__all_sync(FULL, wait(c, &c.o_full[w], st.o_phase, a.status))) return false;
-      st.o_phase ^= 1;
-      tc_fence_after();
+    // the output: every P V is done with the barriers of the two steps behind
+    // the last one (the first of them is not there if there was only one step)
+    if (k + 1 < c.n_items) load_q<D>(a, c.items[k + 1], q);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int buf = (steps + x) & 1;
+      if (steps + x < 2) continue;
+      if (!__all_sync(FULL, wait(c, &c.s_full[w][buf], st.s_phase >> buf & 1, a.status))) return false;
+      st.s_phase ^= 1u << buf;
     }
-    const bool join = !both && hi - it.lo > 1;  // the odd tiles' sums to the first group, through Q's place
-    float* other = reinterpret_cast<float*>(smem + G::kQ);
+    if (!__all_sync(FULL, wait(c, &c.o_full[w], st.o_phase, a.status))) return false;
+    st.o_phase ^= 1;
+    tc_fence_after();
     auto groups_meet = [&]() {
       mbar_arrive(&c.rows_done);
       const bool ok = __all_sync(FULL, wait(c, &c.rows_done, st.done_phase, a.status));
       st.done_phase ^= 1;
       return ok;
     };
+    // 128 rows: the groups' sums over their halves of the slots are joined, each
+    // group writing half of the columns; the other half goes through Q's place
+    const bool join = !both;
+    const int col0 = join ? w * (D / 2) : 0, cols = join ? D / 2 : D;
+    float* mail = reinterpret_cast<float*>(smem + G::kQ);  // [2][D / 2][kTile]
     float f0 = 1.0f, f1 = 0.0f;
     if (join) {
       if (!groups_meet()) return false;  // no MMA reads Q any more
-      if (w == 1) {
-        if (warp_mine) {
+      if (warp_mine) {
+#pragma unroll 1
+        for (int x = 0; x < D / 2; x += 32) {
+          uint32_t o[32];
+          tmem_load(t_o + (w ^ 1) * (D / 2) + x, o);
 #pragma unroll
-          for (int x = 0; x < D; x += 32) {
-            uint32_t o[32];
-            tmem_load(t_o + x, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) other[(x + e) * kTile + r] = __uint_as_float(o[e]);
-          }
+          for (int e = 0; e < 32; ++e) mail[((w ^ 1) * (D / 2) + x + e) * kTile + r] = __uint_as_float(o[e]);
         }
-        c.ml[r] = make_float2(m, l);
       }
+      c.ml[w][r] = make_float2(m, l);
       if (!groups_meet()) return false;
-      if (w == 0) {
-        const float2 ml = c.ml[r];
-        const float top = fmaxf(m, ml.x), z = top == -INFINITY ? 0.0f : top;
-        f0 = ex2(m - z), f1 = ex2(ml.x - z);
-        m = top;
-        l = l * f0 + ml.y * f1;
-      }
+      const float2 ml = c.ml[w ^ 1][r];
+      const float top = fmaxf(m, ml.x), z = top == -INFINITY ? 0.0f : top;
+      f0 = ex2(m - z), f1 = ex2(ml.x - z);
+      m = top;
+      l = l * f0 + ml.y * f1;
     }
     const bool odd = *reinterpret_cast<volatile int*>(&c.bad_v[k]) != 0;
-    if (warp_mine && (both || w == 0)) {
+    if (warp_mine) {
       const float inv = it.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
       uint16_t* dst = a.out + (int64_t)(it.t0 + i) * a.out_stride + (int64_t)(it.h * a.group + g) * D;
 #pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
+      for (int x = col0; x < col0 + cols; x += 32) {
         uint32_t u[32];
         tmem_load(t_o + x, u);
         float o[32];
@@ -768,7 +842,7 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
         for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f0;
         if (join) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] += other[(x + e) * kTile + r] * f1;
+          for (int e = 0; e < 32; ++e) o[e] += mail[(x + e) * kTile + r] * f1;
         }
         if (odd && mine) add_odd_v<D>(a, it, i, g, pos, m, x, o);
         if (mine && it.slot >= 0) {
@@ -785,7 +859,7 @@ __device__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, Ctl& c, RowState&
           }
         }
       }
-      if (mine) {
+      if (mine && col0 == 0) {
         if (it.slot >= 0)
           a.part_ml[(int64_t)it.slot * kRows + local] = make_float2(m, l);
         else if (a.lse)
@@ -861,9 +935,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       mbar_init(&c.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_ready[i], 128);
-      mbar_init(&c.o_full[i], 2);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&c.s_full[i][b], 1);
+        mbar_init(&c.p_ready[i][b], 128);
+      }
+      mbar_init(&c.o_full[i], 1);
     }
     mbar_init(&c.v_go, 1);
     mbar_init(&c.v_ok, 2);
@@ -946,49 +1022,51 @@ constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinCols = kJoinThreads / 32 
 // four columns and eight loads under way, and few parts share an SM.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  constexpr int kWarps = kJoinThreads / 32;
-  __shared__ int slots[kMaxGrid];
-  __shared__ float weight[kMaxGrid][kJoinRows];  // maxima, then the parts' weights
-  __shared__ float sums[kMaxGrid][kJoinRows];
+  constexpr int kWarps = kJoinThreads / 32, kHeld = 8;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, c = blockIdx.x + 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Border& here = a.borders[c];
   const int64_t first = here.first, at = here.at;
   if (at >= first || a.borders[c - 1].first > at || (int)blockIdx.y * kJoinRows >= here.item.rows) return;
-  const int64_t to = at + (here.item.hi - here.item.lo);
-  bool part = false;
-  if (tid < grid - (c - 1)) {
-    part = a.borders[c - 1 + tid].first < to;
-    // a part that begins its item is its CTA's last, the others their CTA's first
-    slots[tid] = tid == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + tid);
-  }
-  const int parts = __syncthreads_count(part);
-  const int row = blockIdx.y * kJoinRows + lane;
-  for (int k = warp; k < parts; k += kWarps) {
-    const float2 ml = a.part_ml[(int64_t)slots[k] * kRows + row];
-    weight[k][lane] = ml.x;
-    sums[k][lane] = ml.y;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int k = 0; k < parts; ++k) top = fmaxf(top, weight[k][lane]);
-  const float z = top == -INFINITY ? 0.0f : top;
-  for (int k = 0; k < parts; ++k) sum += sums[k][lane] * ex2(weight[k][lane] - z);
-  __syncthreads();
-  for (int k = warp; k < parts; k += kWarps) weight[k][lane] = ex2(weight[k][lane] - z);
-  __syncthreads();
   const Item& item = here.item;
-  if (row >= item.rows) return;
-  const int f = item.row0 + row, i = f / a.group, g = f % a.group;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int col = blockIdx.z * kWarps + warp;  // in fours
+  const int64_t to = at + (item.hi - item.lo);
+  const int parts = __syncthreads_count(tid < grid - (c - 1) && a.borders[c - 1 + tid].first < to);
+  const int row = blockIdx.y * kJoinRows + lane, col = blockIdx.z * kWarps + warp;  // columns in fours
   float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-  for (int k = 0; k < parts; ++k) {
-    const float4 p = a.part_o[((int64_t)slots[k] * (D / 4) + col) * kRows + row];
-    const float by = weight[k][lane];
-    o.x += p.x * by, o.y += p.y * by, o.z += p.z * by, o.w += p.w * by;
+  float top = -INFINITY, sum = 0.0f;
+  for (int k0 = 0; k0 < parts; k0 += kHeld) {
+    float2 ml[kHeld];
+    float4 p[kHeld];
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      ml[x] = make_float2(-INFINITY, 0.0f);
+      p[x] = make_float4(0, 0, 0, 0);
+      if (k0 + x < parts) {
+        // a part that begins its item is its CTA's last, the others their CTA's first
+        const int64_t s = 2 * (c - 1 + k0 + x) + (k0 + x == 0 ? 1 : 0);
+        ml[x] = a.part_ml[s * kRows + row];
+        p[x] = a.part_o[(s * (D / 4) + col) * kRows + row];
+      }
+    }
+    float up = top;
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) up = fmaxf(up, ml[x].x);
+    const float z = up == -INFINITY ? 0.0f : up, by = ex2(top - z);
+    o.x *= by, o.y *= by, o.z *= by, o.w *= by;
+    sum *= by;
+    top = up;
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      if (k0 + x >= parts) break;
+      const float f = ex2(ml[x].x - z);
+      o.x += p[x].x * f, o.y += p[x].y * f, o.z += p[x].z * f, o.w += p[x].w * f;
+      sum += ml[x].y * f;
+    }
   }
+  if (row >= item.rows) return;
+  const uint32_t f = item.row0 + row;
+  const int i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
   *reinterpret_cast<uint2*>(dst + col * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   if (col == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
