@@ -15,10 +15,11 @@
 // One CTA per SM, 12 warps:
 //   warp 0      producer: page ids from the block table, K and V tiles by TMA
 //               (one box per page and 64 dims, 128-byte swizzle) into a ring
-//   warp 1      one thread issues the MMAs: S = Q K^T (both from shared
-//               memory) and O += P V (P from tensor memory, V as it lies in
-//               the pages: the MMA takes its B operand with N contiguous)
-//   warps 2-3   in tiles that some row sees in part only: rows of V that lie
+//   warps 1, 2  issue the MMAs, one warp for each group of query rows: S = Q K^T
+//               (both from shared memory) and O += P V (P from tensor memory,
+//               V as it lies in the pages: the MMA takes its B operand with N
+//               contiguous)
+//   warp 3      in tiles that some row sees in part only: rows of V that lie
 //               behind the sequence, or hold an infinity or NaN, are zeroed
 //               before the MMA reads them (0 * NaN would reach every row)
 //   warps 4-11  two groups of 128 threads, a thread per query row: S from
@@ -444,27 +445,29 @@ __device__ __forceinline__ uint32_t o_cols(int w) { return 4 * kPiece + w * 128;
 
 struct MmaState {
   Ring k;                        // the next K or V tile of the ring
-  uint32_t p_phase = 0;          // of p_ready, a bit per group and buffer
+  uint32_t p_phase = 0;          // of p_ready, a bit per buffer
   uint32_t q_phase = 0, v_phase = 0;  // of q_ready, of v_ok
 };
 
-// Step t of group w is a piece of 64 slots: with 256 rows tile t / 2, half
-// t % 2 for both groups, with 128 rows half w of tile t.  S of step t + 2 is
-// made right after O takes step t, whose buffer it reuses; MMAs run in the
-// order of their issue.  s_full[w][t % 2] then says that step t + 2 of S is
-// there and P V of step t is done.
+// The MMAs of group w.  Its step t is a piece of 64 slots: with 256 rows half
+// t % 2 of tile t / 2, with 128 rows half w of tile t.  S of step t + 2 is made
+// right after O takes step t, whose buffer it reuses; the MMAs of a thread run
+// in the order of their issue.  s_full[w][t % 2] then says that step t + 2 of S
+// is there and P V of step t is done.
 //
 // By one whole warp without branches on the lane: an MMA takes its operands
 // from uniform registers, and only code that all lanes run together keeps its
 // addresses there (issued by a lone thread an MMA costs 80 cycles, behind a
 // branch of one lane 45, where it runs 32 or 64).  One elected lane issues.
+// One warp for both groups would spend on barriers and issue what the MMAs of
+// a step take.
 template <int D>
-__device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st) {
+__device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st, const int w) {
   using G = Geo<D>;
   constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kPiece);
   constexpr uint32_t idesc_o = tc_idesc_bf16(kTile, D) | (1u << 16);  // B with N contiguous
   const uint32_t base = smem_u32(smem) >> 4, tmem = uniform(c.tmem), vlo = (G::kHalfBytes >> 4) << 16, klo = 1u << 16;
-  const uint32_t empty = smem_u32(c.empty), s_full = smem_u32(c.s_full);
+  const uint32_t empty = smem_u32(c.empty), s_full = smem_u32(c.s_full[w]);
   const uint32_t lead = elected();
   // The warp's lanes leave every wait together: one that fell behind could
   // miss a phase of a barrier and wait for its parity for good.
@@ -482,61 +485,56 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
     if (!ready(&c.q_ready, st.q_phase)) return false;
     st.q_phase ^= 1;
     tc_fence_after();
+    const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
     for (int t = -2; t < steps; ++t) {
-      const int buf = t & 1;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int half = both ? buf : w;                                          // of step t and of step t + 2
-        const bool fresh = w == 0 && (!both || buf == 0), last = w == 1 && (!both || buf == 1);  // uses of a tile
-        if (t >= 0) {  // O += P V of step t
-          const int x = both ? t >> 1 : t;
-          const bool part = fresh && (x >= masked_from || x < window_to);
-          // This warp waits for every tile of the ring, in order (a barrier's
-          // parity tells neighbouring phases apart, not those two laps apart),
-          // and sends the tiles that need it to clean_v.
-          if (fresh && !ready(&c.full[vpos.stage], vpos.phase)) return false;
-          if (part) arrive_if(lead, smem_u32(&c.v_go));
-          if (!ready(&c.p_ready[w][buf], st.p_phase >> (w * 2 + buf) & 1)) return false;
-          st.p_phase ^= 1u << (w * 2 + buf);
-          if (part) {
-            if (!ready(&c.v_ok, st.v_phase)) return false;
-            st.v_phase ^= 1;
-          }
-          tc_fence_after();
-          const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | vlo;
-          const uint32_t td = tmem + o_cols(w), ta = tmem + s_cols(w, buf);
-#pragma unroll
-          for (int e = 0; e < kPiece / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
-            mma_ts_if(lead, td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, t > 0 || e > 0);
-          if (last) {
-            commit_if(lead, empty + vpos.stage * 8);
-            vpos.advance<G::kStages>();
-            vpos.advance<G::kStages>();
-          }
+      const int buf = t & 1, half = both ? buf : w;          // of step t and of step t + 2
+      const bool fresh = !both || buf == 0, last = !both || buf == 1;  // the group's first, its last use of a tile
+      if (t >= 0) {  // O += P V of step t
+        const int x = both ? t >> 1 : t;
+        const bool part = fresh && (x >= masked_from || x < window_to);
+        // Both warps wait for every tile of the ring, in order (a barrier's
+        // parity tells neighbouring phases apart, not those two laps apart),
+        // and send the tiles that need it to clean_v.
+        if (fresh && !ready(&c.full[vpos.stage], vpos.phase)) return false;
+        if (part) arrive_if(lead, smem_u32(&c.v_go));
+        if (!ready(&c.p_ready[w][buf], st.p_phase >> buf & 1)) return false;
+        st.p_phase ^= 1u << buf;
+        if (part) {
+          if (!ready(&c.v_ok, st.v_phase)) return false;
+          st.v_phase ^= 1;
         }
-        if (t + 2 < steps) {  // S = Q K^T of step t + 2
-          if (fresh && !ready(&c.full[kpos.stage], kpos.phase)) return false;
-          tc_fence_after();
-          const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
-          const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | klo;
-          const uint32_t ts = tmem + s_cols(w, buf);
+        tc_fence_after();
+        const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | vlo;
+        const uint32_t td = tmem + o_cols(w), ta = tmem + s_cols(w, buf);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
-            mma_ss_if(lead, ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
-          }
-          if (last) {
-            commit_if(lead, empty + kpos.stage * 8);
-            kpos.advance<G::kStages>();
-            kpos.advance<G::kStages>();
-          }
+        for (int e = 0; e < kPiece / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
+          mma_ts_if(lead, td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, t > 0 || e > 0);
+        if (last) {
+          commit_if(lead, empty + vpos.stage * 8);
+          vpos.advance<G::kStages>();
+          vpos.advance<G::kStages>();
         }
-        if (t >= 0 || t + 2 < steps) commit_if(lead, s_full + (w * 2 + buf) * 8);
       }
+      if (t + 2 < steps) {  // S = Q K^T of step t + 2
+        if (fresh && !ready(&c.full[kpos.stage], kpos.phase)) return false;
+        tc_fence_after();
+        const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | klo;
+        const uint32_t ts = tmem + s_cols(w, buf);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
+          mma_ss_if(lead, ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
+        }
+        if (last) {
+          commit_if(lead, empty + kpos.stage * 8);
+          kpos.advance<G::kStages>();
+          kpos.advance<G::kStages>();
+        }
+      }
+      if (t >= 0 || t + 2 < steps) commit_if(lead, s_full + buf * 8);
     }
-    // what this warp has seen (clean_v's word on the item), to the groups
-    arrive_if(lead, smem_u32(&c.o_full[0]));
-    arrive_if(lead, smem_u32(&c.o_full[1]));
+    // what this warp has seen (clean_v's word on the item), to the group
+    arrive_if(lead, smem_u32(&c.o_full[w]));
     st.k = kpos;  // two positions per tile: behind the item's last V
   }
   return true;
@@ -551,7 +549,7 @@ struct CleanState {
 template <int D>
 __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st) {
   using G = Geo<D>;
-  const int tid = threadIdx.x - 64;
+  const int lane = threadIdx.x % 32;
   for (int k = 0; k < c.n_items; ++k) {
     const Item it = c.items[k];
     for (int j = it.lo; j < it.hi; ++j) {
@@ -560,7 +558,7 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
         if (!__all_sync(FULL, wait(c, &c.v_go, st.phase, a.status))) return false;
         st.phase ^= 1;
         const uint32_t tile = smem_u32(smem + G::kRing + st.k.stage * G::kTileBytes);
-        for (int row = tid; row < kTile; row += 64) {
+        for (int row = lane; row < kTile; row += 32) {
           bool drop = j * kTile + row >= it.ctx + it.n;
           if (!drop) {
             uint32_t odd = 0;  // exponents all ones
@@ -584,7 +582,7 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (tid % 32 == 0) mbar_arrive(&c.v_ok);
+        if (lane == 0) mbar_arrive(&c.v_ok);
       }
       st.k.advance<G::kStages>();  // V
     }
@@ -913,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   using G = Geo<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl& c = *reinterpret_cast<Ctl*>(smem + G::kCtl);
-  const int tid = threadIdx.x, warp = tid / 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Load load;
   if (warp == 0) {
@@ -932,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     c.abort = 0;
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       for (int b = 0; b < 2; ++b) {
@@ -941,11 +939,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       mbar_init(&c.o_full[i], 1);
     }
-    mbar_init(&c.v_go, 1);
-    mbar_init(&c.v_ok, 2);
+    mbar_init(&c.v_go, 2);
+    mbar_init(&c.v_ok, 1);
     mbar_init(&c.q_ready, 256);
     mbar_init(&c.rows_done, 256);
-    mbar_init(&c.drain, 1);
+    mbar_init(&c.drain, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -969,9 +967,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       __syncthreads();
       if (warp == 0)
         ok = produce<D>(a, smem, c, fill, filled);
-      else if (warp == 1)
-        ok = issue_mmas<D>(a, smem, c, mma);
-      else if (warp >= 2)
+      else if (warp < 3)
+        ok = issue_mmas<D>(a, smem, c, mma, warp - 1);
+      else
         ok = clean_v<D>(a, smem, c, check);
       ok = __syncthreads_and(ok);
       u = c.next;
@@ -999,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
       }
     }
-    if (warp == 1 && elected()) {  // the lane that issued the MMAs
+    if ((warp == 1 || warp == 2) && elected()) {  // the lanes that issued the MMAs
       tc_commit(&c.drain);
       for (int64_t until = gtimer() + kWaitNs; !mbar_try_wait(&c.drain, 0) && gtimer() < until;) {
       }
