@@ -431,18 +431,19 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows > 65535) return fail(MK_ERR_ARG, "more than 65535 rows of logits");
   constexpr int smem = (int)sizeof(Joined);
-  if (cudaFuncSetAttribute(select_join, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return launched("select");
+  static std::atomic<uint64_t> join_ready{0}, wide_ready{0};
+  int rc = allow_smem(join_ready, reinterpret_cast<const void*>(&select_join), smem, "select");
+  if (rc != MK_OK) return rc;
   const dim3 grid((unsigned)a.parts, (unsigned)rows);
   if (n_out <= 32) {
     select_parts<32><<<grid, kThreads, kWarps * sizeof(Best<32>), st>>>(a);
   } else {
     constexpr int wide = (int)(kWarps * sizeof(Best<kMaxOut>));
-    if (cudaFuncSetAttribute(select_parts<kMaxOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide) != cudaSuccess)
-      return launched("select");
+    rc = allow_smem(wide_ready, reinterpret_cast<const void*>(&select_parts<kMaxOut>), wide, "select");
+    if (rc != MK_OK) return rc;
     select_parts<kMaxOut><<<grid, kThreads, wide, st>>>(a);
   }
-  const int rc = launched("select");
+  rc = launched("select");
   if (rc != MK_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)requests);

@@ -335,6 +335,7 @@ int encode_pools(mk_kv* kv) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  if (kv->tm_ready) return MK_OK;
   std::lock_guard<std::mutex> hold(kv->tm_lock);
   if (kv->tm_ready) return MK_OK;
   void* f = nullptr;

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 #include <string>
 
@@ -19,7 +20,7 @@ struct mk_kv {
   uint64_t freq[64] = {};
   // tensor maps of the pools, made by the first call that reads through them
   std::mutex tm_lock;
-  bool tm_ready = false;
+  std::atomic<bool> tm_ready{false};
   CUtensorMap tm_k, tm_v;
 };
 
@@ -93,6 +94,21 @@ inline size_t span(int64_t rows, int64_t stride, int64_t row_elems, size_t elem)
 inline int launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+  return MK_OK;
+}
+
+// A kernel's shared memory limit, raised once per device (the call costs about
+// as much as a launch).  done: a bit per device of one kernel.
+inline int allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes, const char* what) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return MK_OK;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(MK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  }
+  if (dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   return MK_OK;
 }
 

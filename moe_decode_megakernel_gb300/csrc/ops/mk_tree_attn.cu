@@ -19,9 +19,9 @@
 //               (both from shared memory) and O += P V (P from tensor memory,
 //               V as it lies in the pages: the MMA takes its B operand with N
 //               contiguous)
-//   warp 3      in tiles that some row sees in part only: rows of V that lie
-//               behind the sequence, or hold an infinity or NaN, are zeroed
-//               before the MMA reads them (0 * NaN would reach every row)
+//   warp 3      rows of V that lie behind the sequence, or that only some rows
+//               see and that hold an infinity or NaN, are zeroed before the
+//               MMA reads them (0 * NaN would reach every row)
 //   warps 4-11  two groups of 128 threads, a thread per query row: S from
 //               tensor memory, the running maximum and sum, P back as bf16
 // The two groups take the two halves of 256 query rows, or, where an item has
@@ -78,7 +78,7 @@ struct Item {
   int b, h, t0, n, ctx;        // sequence, K/V head, its first token row, new tokens, cached
   int row0, rows;              // query rows of the K/V head: first, count (1 .. kRows)
   int lo, hi;                  // tiles of this part
-  int masked_from, window_to;  // tiles >= the one or < the other may be masked in part
+  int masked_from, window_to;  // slots >= the one or < the other may be masked for some rows
   int slot;                    // workspace slot of the part, -1: the item is whole
 };
 
@@ -190,11 +190,10 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
   it.rows = s.n * a.group - it.row0 < kRows ? s.n * a.group - it.row0 : kRows;
   tiles_of(a, s, m, it.lo, it.hi);
   const int i0 = (uint32_t)it.row0 / (uint32_t)a.group, i1 = (uint32_t)(it.row0 + it.rows - 1) / (uint32_t)a.group;
-  it.masked_from = (s.ctx + (a.mask ? 0 : i0 + 1)) / kTile;
+  it.masked_from = s.ctx + (a.mask ? 0 : i0 + 1);
   it.window_to = 0;
   if (a.window) {
-    const int first = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
-    if (first > 0) it.window_to = (first + kTile - 1) / kTile;
+    it.window_to = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
   }
   it.slot = -1;
   return it;
@@ -274,7 +273,11 @@ struct Ring {
 };
 
 __device__ __forceinline__ bool both_in(const Item& it) { return it.rows > kTile; }
-__device__ __forceinline__ bool in_part(const Item& it, int j) { return j >= it.masked_from || j < it.window_to; }
+// Whether tile j holds slots behind the sequence or masked for some rows.
+__device__ __forceinline__ bool in_part(int masked_from, int window_to, int j) {
+  return (j + 1) * kTile > masked_from || j * kTile < window_to;
+}
+__device__ __forceinline__ bool in_part(const Item& it, int j) { return in_part(it.masked_from, it.window_to, j); }
 
 // ------------------------------------------------------------- visibility
 
@@ -477,7 +480,7 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
     const Item& it = c.items[k];
     const bool both = uniform(both_in(it));
     const int lo = uniform(it.lo), tiles = uniform(it.hi) - lo;
-    const int masked_from = uniform(it.masked_from) - lo, window_to = uniform(it.window_to) - lo;
+    const int masked_from = uniform(it.masked_from) - lo * kTile, window_to = uniform(it.window_to) - lo * kTile;
     const int steps = both ? 2 * tiles : tiles;
     // tile x of the item: K at ring position 2x, V at 2x + 1 from here on
     Ring kpos = st.k, vpos = st.k;
@@ -491,7 +494,7 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
       const bool fresh = !both || buf == 0, last = !both || buf == 1;  // the group's first, its last use of a tile
       if (t >= 0) {  // O += P V of step t
         const int x = both ? t >> 1 : t;
-        const bool part = fresh && (x >= masked_from || x < window_to);
+        const bool part = fresh && in_part(masked_from, window_to, x);
         // Both warps wait for every tile of the ring, in order (a barrier's
         // parity tells neighbouring phases apart, not those two laps apart),
         // and send the tiles that need it to clean_v.
@@ -558,10 +561,12 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
         if (!__all_sync(FULL, wait(c, &c.v_go, st.phase, a.status))) return false;
         st.phase ^= 1;
         const uint32_t tile = smem_u32(smem + G::kRing + st.k.stage * G::kTileBytes);
+        const int len = it.ctx + it.n, s0 = j * kTile;
         for (int row = lane; row < kTile; row += 32) {
-          bool drop = j * kTile + row >= it.ctx + it.n;
-          if (!drop) {
+          bool drop = s0 + row >= len;
+          if (!drop && (s0 + row >= it.masked_from || s0 + row < it.window_to)) {
             uint32_t odd = 0;  // exponents all ones
+#pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
               const uint4 u = lds128(tile + ch / 8 * G::kHalfBytes + row * 128 + ((ch % 8) ^ (row & 7)) * 16);
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -575,6 +580,7 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
             }
           }
           if (drop)
+#pragma unroll
             for (int ch = 0; ch < D / 8; ++ch)
               asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + ch / 8 * G::kHalfBytes + row * 128 + ch % 8 * 16),
                            "r"(0u)
@@ -640,7 +646,7 @@ __device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int
   for (int j = it.lo; j < it.hi; ++j) {
     if (!in_part(it, j)) continue;
     for (int s = j * kTile; s < min((j + 1) * kTile, it.ctx + it.n); ++s) {
-      if (!(seen(a, it, i, pos, s) & 1)) continue;
+      if ((s < it.masked_from && s >= it.window_to) || !(seen(a, it, i, pos, s) & 1)) continue;
       const int64_t row = pool_row(a, it, s) * D;
       bool odd = false;
       float dot = 0;
@@ -722,7 +728,7 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
       const uint32_t t_s = lane_base + s_cols(w, buf);
       uint32_t s[kPiece];
       tmem_load(t_s, s);
-      if (j >= masked_from || j < window_to) {
+      if (in_part(masked_from, window_to, j)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint32_t v = seen(a, it, i, pos, j * kTile + (both ? buf : w) * kPiece + x * 32);
@@ -1078,10 +1084,11 @@ template <int D>
 int launch(const AttnArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = Geo<D>::kCtl + (int)sizeof(Ctl);
   static_assert(smem <= 232448, "shared memory of a block");
-  const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string("tree_attn: ") + cudaGetErrorString(e));
+  static std::atomic<uint64_t> ready{0};
+  int rc = allow_smem(ready, reinterpret_cast<const void*>(&attn_kernel<D>), smem, "tree_attn");
+  if (rc != MK_OK) return rc;
   attn_kernel<D><<<grid, kThreads, smem, st>>>(a);
-  const int rc = launched("tree_attn");
+  rc = launched("tree_attn");
   if (rc != MK_OK || grid == 1) return rc;
   // the join may be resident (waiting) before the last parts are written
   const int64_t rows = (int64_t)a.b.n_tokens * a.group;
@@ -1137,12 +1144,11 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   if (!(io->scale >= 0) || !std::isfinite(io->scale)) return fail(MK_ERR_ARG, "scale must be positive (0: 1 / sqrt(head_dim))");
   if (!workspace || misaligned(workspace)) return fail(MK_ERR_ARG, "workspace null or misaligned");
   if (tok->batch == 0 || tok->n_tokens == 0) return MK_OK;
-  const size_t need = mk_tree_attn_workspace_bytes(kv);
-  if (need == 0) return fail(MK_ERR_CUDA, "no device");
-  if (workspace_bytes < need) return fail(MK_ERR_ARG, "workspace smaller than mk_tree_attn_workspace_bytes");
+  const int grid = grid_size();
+  if (grid < 1) return fail(MK_ERR_CUDA, "no device");
+  if (workspace_bytes < part_bytes(grid, c.head_dim)) return fail(MK_ERR_ARG, "workspace smaller than mk_tree_attn_workspace_bytes");
   rc = encode_pools(kv);
   if (rc != MK_OK) return rc;
-  const int grid = grid_size();
   AttnArgs a;
   a.pools = pools_of(kv, layer);
   a.b = batch_of(tok);
