@@ -1,16 +1,18 @@
 // mk_tree_attn.cu -- attention of new tokens (a drafted tree, or a run) over
 // the paged pools, on the tcgen05 tensor cores.
 //
-// The work is cut into units: 128 slots of K and V of one (sequence, K/V head)
+// The work is cut into tiles: 128 slots of K and V of one (sequence, K/V head)
 // against one group of up to 256 query rows.  A query row is a (token, query
 // head) pair of the K/V head, in the order token * group + head, so that the
-// rows of a tree share each K/V tile that is read.  All units, in the order
-// (sequence, head, query group, tile), are dealt to the SMs in equal runs: a
-// long context is split over many SMs, a short one costs no more than it
-// holds, and nothing about the lengths is known to the host.  Where an item
-// (all tiles of one query group) is cut by the border between two SMs, each
-// leaves its part (row maxima, sums, unnormalised outputs, fp32) in the
-// workspace and a second kernel joins the parts in order.
+// rows of a tree share each K/V tile that is read.  All tiles, in the order
+// (sequence, head, query group, tile), are dealt to the SMs in runs of equal
+// cost: a unit for each tile, and for the opening of each item (all tiles of
+// one query group) what the fill and the drain of the pipeline and the output
+// cost (see opening_of).  So a long
+// context is split over many SMs, a short one costs no more than it holds, and
+// nothing about the lengths is known to the host.  Where an item is cut by the
+// border between two SMs, each leaves its part (row maxima, sums, unnormalised
+// outputs, fp32) in the workspace and a second kernel joins the parts in order.
 //
 // One CTA per SM, 12 warps:
 //   warp 0      producer: page ids from the block table, K and V tiles by TMA
@@ -60,6 +62,7 @@ constexpr int kTile = 128;               // slots of a K/V tile, rows of an MMA
 constexpr int kPiece = kTile / 2;        // slots of a piece of S
 constexpr int kRows = 2 * kTile;         // query rows of an item
 constexpr int kThreads = 384;
+constexpr int kOpenOne = 3, kOpenBoth = 1;  // see opening_of
 constexpr int kMaxItems = 8;             // items planned at a time
 constexpr float kSlack = 8.0f;           // log2: how far the maximum in use may lag
 constexpr int64_t kWaitNs = 2000000000;  // a wait that takes longer is given up
@@ -82,8 +85,8 @@ struct Item {
   int slot;                    // workspace slot of the part, -1: the item is whole
 };
 
-// Where a CTA's units begin: its first unit, and the whole item that holds it
-// (beginning at unit `at`; at = first where the CTA has none).
+// Where a CTA's units begin: its first unit, and the first whole item that it
+// has tiles of (its first tile at unit `at`; at = first where there is none).
 struct Border {
   int64_t first, at;
   Item item;
@@ -92,7 +95,7 @@ struct Border {
 struct Ctl {
   uint64_t full[8], empty[8], s_full[2][2], p_ready[2][2], o_full[2], v_go, v_ok, q_ready, rows_done, drain;
   uint32_t tmem, abort;
-  int n_items, ok;
+  int n_items;
   int64_t first, end;  // this CTA's units
   int64_t next;
   int bad_v[kMaxItems];  // an infinity or NaN was zeroed in one of the item's tiles
@@ -124,19 +127,27 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Seq& s, int m,
   }
 }
 
+// Units before the first tile of query group m: what a further item costs an
+// SM beside its tiles, about 4 us, in tiles of 1.2 us (up to 128 rows, bound by
+// memory) or 2 us.  None where every SM has a tile at most: an item is one
+// SM's first anyway.
+__device__ __forceinline__ int opening_of(const AttnArgs& a, const Seq& s, int m, bool many) {
+  return !many ? 0 : s.n * a.group - m * kRows > kTile ? kOpenBoth : kOpenOne;
+}
+
 __device__ __forceinline__ int groups_of(const AttnArgs& a, const Seq& s) {
   return (s.n * a.group - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
 
-// Units of one K/V head of a sequence.
-__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Seq& s) {
-  int64_t u = 0;
+// Tiles of one K/V head of a sequence, and the units of their openings.
+__device__ __forceinline__ void units_of(const AttnArgs& a, const Seq& s, int64_t& tiles, int64_t& open) {
+  tiles = open = 0;
   for (int m = 0, M = groups_of(a, s); m < M; ++m) {
     int lo, hi;
     tiles_of(a, s, m, lo, hi);
-    u += hi - lo;
+    tiles += hi - lo;
+    open += opening_of(a, s, m, true);
   }
-  return u;
 }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
@@ -154,25 +165,34 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of numbers
 // A lane's sequence of a round of 32, and the units of one of its heads.
 struct Load {
   Seq s;
-  int64_t per_head;
+  int64_t tiles, open;
 };
 __device__ __forceinline__ Load load_of(const AttnArgs& a, int b) {
-  Load x = {{0, 0, 0}, 0};
+  Load x = {{0, 0, 0}, 0, 0};
   if (b < a.b.batch) {
     x.s = attn_seq(a, b);
-    x.per_head = units_of(a, x.s);
+    units_of(a, x.s, x.tiles, x.open);
   }
   return x;
 }
 
-// All units (by one warp), and the lane's sequence of the first round.
-__device__ __forceinline__ int64_t total_units(const AttnArgs& a, Load& first) {
+// All units (by one warp), whether they count openings, and the lane's
+// sequence of the first round.
+__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int grid, Load& first, bool& many) {
   const int lane = threadIdx.x % 32;
   first = load_of(a, lane);
-  int64_t u = first.per_head;
-  for (int b = lane + 32; b < a.b.batch; b += 32) u += load_of(a, b).per_head;
-  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
-  return u * a.pools.n_kv;
+  int64_t u = first.tiles, v = first.open;
+  for (int b = lane + 32; b < a.b.batch; b += 32) {
+    const Load x = load_of(a, b);
+    u += x.tiles;
+    v += x.open;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    u += __shfl_xor_sync(FULL, u, o);
+    v += __shfl_xor_sync(FULL, v, o);
+  }
+  many = u * a.pools.n_kv > grid;
+  return (u + (many ? v : 0)) * a.pools.n_kv;
 }
 
 // The first unit of CTA c: even runs, the longer ones first.
@@ -199,17 +219,17 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
   return it;
 }
 
-// Calls f(item, first unit of the item) for the items that hold units [u, end),
-// in order, while it returns true.  By one warp, whose lanes hold the first
+// Calls f(item, unit of the item's first tile) for the items whose tiles lie in
+// units [u, end), in order, while it returns true.  By one warp, whose lanes hold the first
 // round's sequences; f runs on every lane.
 template <typename F>
-__device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, int64_t u, int64_t end, F f) {
+__device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, bool many, int64_t u, int64_t end, F f) {
   const int lane = threadIdx.x % 32;
   int64_t base = 0;  // units before this round of sequences
   for (int b0 = 0; b0 < a.b.batch && base < end; b0 += 32) {
     const Load x = b0 == 0 ? first : load_of(a, b0 + lane);
     const Seq s = x.s;
-    const int64_t per_head = x.per_head;
+    const int64_t per_head = x.tiles + (many ? x.open : 0);
     const int64_t incl = warp_scan(per_head * a.pools.n_kv);
     uint32_t hit = __ballot_sync(FULL, per_head > 0 && base + incl > u && base + incl - per_head * a.pools.n_kv < end);
     while (hit) {
@@ -225,6 +245,7 @@ __device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, 
         for (int m = 0; m < M; ++m) {
           int lo, hi;
           tiles_of(a, q, m, lo, hi);
+          at += opening_of(a, q, m, many);
           if (at + (hi - lo) > u) {
             if (at >= end) return;
             if (!f(make_item(a, q, b0 + src, h, m), at)) return;
@@ -282,11 +303,11 @@ __device__ __forceinline__ bool in_part(const Item& it, int j) { return in_part(
 // ------------------------------------------------------------- visibility
 
 // Bits of the new tokens j0 .. j0 + 31 in a token's mask row (j0 > -32; bits
-// below token 0 are clear).
-__device__ __forceinline__ uint32_t mask_bits(const uint64_t* row, int words, int j0) {
-  if (j0 < 0) return (uint32_t)(row[0] << -j0);
+// below token 0 are clear), whose first word is at hand.
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* row, uint64_t word0, int words, int j0) {
+  if (j0 < 0) return (uint32_t)(word0 << -j0);
   const int w = j0 >> 6, sh = j0 & 63;
-  uint64_t v = w < words ? row[w] >> sh : 0;
+  uint64_t v = w == 0 ? word0 >> sh : w < words ? row[w] >> sh : 0;
   if (sh > 32 && w + 1 < words) v |= row[w + 1] << (64 - sh);
   return (uint32_t)v;
 }
@@ -303,7 +324,7 @@ __device__ __forceinline__ int position_of(const AttnArgs& a, const Item& it, in
 }
 
 // Which of the slots s0 .. s0 + 31 token i sees.
-__device__ __forceinline__ uint32_t seen(const AttnArgs& a, const Item& it, int i, int pos, int s0) {
+__device__ __forceinline__ uint32_t seen(const AttnArgs& a, const Item& it, int i, int pos, uint64_t word0, int s0) {
   const int len = it.ctx + it.n;
   if (s0 >= len) return 0;
   uint32_t v = FULL;
@@ -312,7 +333,7 @@ __device__ __forceinline__ uint32_t seen(const AttnArgs& a, const Item& it, int 
   if (j0 > -32) {
     uint32_t d;
     if (a.mask) {
-      d = mask_bits(a.mask + (int64_t)(it.t0 + i) * a.mask_words, a.mask_words, j0);
+      d = mask_bits(a.mask + (int64_t)(it.t0 + i) * a.mask_words, word0, a.mask_words, j0);
       if (j0 < 0) d |= (1u << -j0) - 1;
     } else {
       const int k = i + 1 - j0;  // tokens from j0 up to i
@@ -582,7 +603,7 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
           if (drop)
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + ch / 8 * G::kHalfBytes + row * 128 + ch % 8 * 16),
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + ch / 8 * G::kHalfBytes + row * 128 + ((ch % 8) ^ (row & 7)) * 16),
                            "r"(0u)
                            : "memory");
         }
@@ -641,12 +662,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // What clean_v zeroed, for the rows that see it: its products with the row's
 // probabilities, added to 32 columns of the row's output.
 template <int D>
-__device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int i, int g, int pos, float m, int col, float (&o)[32]) {
+__device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int i, int g, int pos, uint64_t word0, float m, int col, float (&o)[32]) {
   const uint16_t* q = a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D;
   for (int j = it.lo; j < it.hi; ++j) {
     if (!in_part(it, j)) continue;
     for (int s = j * kTile; s < min((j + 1) * kTile, it.ctx + it.n); ++s) {
-      if ((s < it.masked_from && s >= it.window_to) || !(seen(a, it, i, pos, s) & 1)) continue;
+      if ((s < it.masked_from && s >= it.window_to) || !(seen(a, it, i, pos, word0, s) & 1)) continue;
       const int64_t row = pool_row(a, it, s) * D;
       bool odd = false;
       float dot = 0;
@@ -714,6 +735,7 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
     const uint32_t f = it.row0 + (mine ? local : 0);
     const int i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
     const int pos = a.window ? position_of(a, it, i) : 0;
+    const uint64_t word0 = a.mask ? a.mask[(int64_t)(it.t0 + i) * a.mask_words] : 0;
     float m = -INFINITY, l = 0.0f;
     const int lo = it.lo, steps = both ? 2 * (it.hi - lo) : it.hi - lo, masked_from = it.masked_from, window_to = it.window_to;
     for (int t = 0; t < steps; ++t) {
@@ -731,7 +753,7 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
       if (in_part(masked_from, window_to, j)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint32_t v = seen(a, it, i, pos, j * kTile + (both ? buf : w) * kPiece + x * 32);
+          const uint32_t v = seen(a, it, i, pos, word0, j * kTile + (both ? buf : w) * kPiece + x * 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((v >> e) & 1)) s[x * 32 + e] = 0xff800000u;
@@ -848,7 +870,7 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] += mail[(x + e) * kTile + r] * f1;
         }
-        if (odd && mine) add_odd_v<D>(a, it, i, g, pos, m, x, o);
+        if (odd && mine) add_odd_v<D>(a, it, i, g, pos, word0, m, x, o);
         if (mine && it.slot >= 0) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -877,11 +899,11 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
 }
 
 // The next items of a CTA's units [u, end), which began at `begin` (by one warp).
-__device__ __forceinline__ void plan_items(const AttnArgs& a, Ctl& c, const Load& first, int64_t begin, int64_t u, int64_t end) {
+__device__ __forceinline__ void plan_items(const AttnArgs& a, Ctl& c, const Load& first, bool many, int64_t begin, int64_t u, int64_t end) {
   const bool one = threadIdx.x % 32 == 0;
   int n = 0;
   int64_t next = end;
-  each_item(a, first, u, end, [&](Item it, int64_t at) {
+  each_item(a, first, many, u, end, [&](Item it, int64_t at) {
     if (one && u == begin && n == 0) {
       a.borders[blockIdx.x].at = at;
       a.borders[blockIdx.x].item = it;
@@ -919,45 +941,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   Ctl& c = *reinterpret_cast<Ctl*>(smem + G::kCtl);
   const int tid = threadIdx.x, warp = uniform(tid / 32);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Load load;
-  if (warp == 0) {
-    const int64_t total = total_units(a, load);
+  if ((smem_u32(smem) & 1023) != 0) {  // the MMAs' layouts count on it
     if (tid == 0) {
-      c.first = border(total, blockIdx.x, gridDim.x);
-      c.end = border(total, blockIdx.x + 1, gridDim.x);
-      a.borders[blockIdx.x].first = c.first;
-      a.borders[blockIdx.x].at = c.first;  // until the plan says more
+      record(a.status, ERR_SMEM_ALIGN, OP_ATTN, 0, 0, smem_u32(smem), 1024);
+      a.borders[blockIdx.x].first = a.borders[blockIdx.x].at = 0;
+      if (blockIdx.x == 0) a.borders[gridDim.x].first = 0;
+    }
+    return;
+  }
+  Load load;
+  bool many = false;
+  int64_t u = 0, end = 0;
+  if (warp == 0) {  // this CTA's units, and its first items
+    const int64_t total = total_units(a, gridDim.x, load, many);
+    u = border(total, blockIdx.x, gridDim.x);
+    end = border(total, blockIdx.x + 1, gridDim.x);
+    if (tid == 0) {
+      c.first = u;
+      c.end = end;
+      a.borders[blockIdx.x].first = u;
+      a.borders[blockIdx.x].at = u;  // until the plan says more
       if (blockIdx.x == 0) a.borders[gridDim.x].first = total;
     }
-  }
-  if (tid == 0) {
-    c.ok = (smem_u32(smem) & 1023) == 0;
-    if (!c.ok) record(a.status, ERR_SMEM_ALIGN, OP_ATTN, 0, 0, smem_u32(smem), 1024);
-    c.abort = 0;
-    for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&c.s_full[i][b], 1);
-        mbar_init(&c.p_ready[i][b], 128);
+    plan_items(a, c, load, many, u, u, end);
+  } else if (warp == 1) {
+    if (tid == 32) {
+      c.abort = 0;
+      for (int i = 0; i < G::kStages; ++i) {
+        mbar_init(&c.full[i], 1);
+        mbar_init(&c.empty[i], 2);
       }
-      mbar_init(&c.o_full[i], 1);
+      for (int i = 0; i < 2; ++i) {
+        for (int b = 0; b < 2; ++b) {
+          mbar_init(&c.s_full[i][b], 1);
+          mbar_init(&c.p_ready[i][b], 128);
+        }
+        mbar_init(&c.o_full[i], 1);
+      }
+      mbar_init(&c.v_go, 2);
+      mbar_init(&c.v_ok, 1);
+      mbar_init(&c.q_ready, 256);
+      mbar_init(&c.rows_done, 256);
+      mbar_init(&c.drain, 2);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    mbar_init(&c.v_go, 2);
-    mbar_init(&c.v_ok, 1);
-    mbar_init(&c.q_ready, 256);
-    mbar_init(&c.rows_done, 256);
-    mbar_init(&c.drain, 2);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    tmem_alloc(&c.tmem, 512);
   }
   __syncthreads();
-  int64_t u = c.first;
-  const int64_t begin = u, end = c.end;
-  if (u >= end || !c.ok) return;
-  if (warp == 1) tmem_alloc(&c.tmem, 512);
-  __syncthreads();
+  const int64_t begin = c.first;
+  u = begin, end = c.end;
 
   // The softmax warps keep a row of S in registers: the other warps hand them
   // theirs (128 x 80 + 256 x 208 of the launch's 384 x 168).
@@ -969,8 +1002,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     CleanState check;
     MmaState mma;
     while (u < end && ok) {
-      if (warp == 0) plan_items(a, c, load, begin, u, end);
-      __syncthreads();
+      if (u > begin) {
+        if (warp == 0) plan_items(a, c, load, many, begin, u, end);
+        __syncthreads();
+      }
       if (warp == 0)
         ok = produce<D>(a, smem, c, fill, filled);
       else if (warp < 3)
@@ -985,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     RowState rows;
     while (u < end && ok) {
-      __syncthreads();
+      if (u > begin) __syncthreads();
       ok = softmax_rows<D>(a, smem, c, rows);
       ok = __syncthreads_and(ok);
       u = c.next;

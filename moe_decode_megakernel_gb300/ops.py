@@ -46,12 +46,13 @@ class MkAttnIo(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("n_q", "mask_words", "window")] + [("scale", ctypes.c_float)]
 
 
-_L = None
+_L = torch = None  # loaded by the first call: the package is imported without torch
 
 
 def _lib():
-    global _L
+    global _L, torch
     if _L is None:
+        import torch
         L = lib()
         vp, i32, i64, sz, p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER
         sig = {
@@ -101,7 +102,6 @@ def _rows(t, name: str, dtype, shape, device):
 
 def _call(fn, device, stream, *args) -> None:
     """fn(*args, raw stream) with the tensors' device current."""
-    import torch
     if device.type != "cuda":
         _bad(f"tensors on {device}: a CUDA device is wanted")
     if stream is None:
@@ -124,7 +124,7 @@ class KvCache:
     and the rotation's base.  Keeps the tensors alive."""
 
     def __init__(self, k_pool, v_pool, rope_base: float = 500000.0):
-        import torch
+        _lib()
         for t in (k_pool, v_pool):
             if t.dim() != 5 or t.shape != k_pool.shape or not t.is_contiguous() or t.device != k_pool.device or \
                     t.dtype not in (torch.bfloat16, torch.uint16):
@@ -145,7 +145,6 @@ class KvCache:
 
 
 def _tokens(cache, n_tokens, cu_seqlens, cache_lens, block_tables, positions):
-    import torch
     i32, dev = torch.int32, cache.device
     batch, max_pages = cache_lens.shape[0], block_tables.shape[-1]
     return MkTokens(batch, n_tokens, max_pages, _take(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
@@ -155,7 +154,6 @@ def _tokens(cache, n_tokens, cu_seqlens, cache_lens, block_tables, positions):
 
 
 def _status(status, device):
-    import torch
     return _take(status, "status", torch.int32, (8,), device)
 
 
@@ -164,21 +162,21 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
     """mk_kv_append: k and v [tokens][n_kv][head_dim] (bf16 or fp32) into
     `layer` of the pools, k rotated; q [tokens][n_q][head_dim] of the same type
     rotated into q_out (bf16)."""
-    import torch
     dev, T, d = cache.device, k.shape[0], cache.head_dim
     if k.dtype not in (torch.bfloat16, torch.float32):
         _bad(f"k: bf16 or fp32 is wanted, got {k.dtype}")
-    io = MkAppendIo(dtype=MK_F32 if k.dtype is torch.float32 else MK_BF16)
-    io.k, io.k_stride = _rows(k, "k", k.dtype, (T, cache.n_kv, d), dev)
-    io.v, io.v_stride = _rows(v, "v", k.dtype, (T, cache.n_kv, d), dev)
+    kp, ks = _rows(k, "k", k.dtype, (T, cache.n_kv, d), dev)
+    vp, vs = _rows(v, "v", k.dtype, (T, cache.n_kv, d), dev)
     if (q is None) != (q_out is None):
         _bad("q and q_out go together")
+    qp = qs = op = os_ = n_q = 0
     if q is not None:
         if q.dim() != 3 or q.shape[1] < 1:
             _bad(f"q: [tokens][heads][head_dim] is wanted, got {tuple(q.shape)}")
-        io.n_q = q.shape[1]
-        io.q, io.q_stride = _rows(q, "q", k.dtype, (T, io.n_q, d), dev)
-        io.q_out, io.q_out_stride = _rows(q_out, "q_out", torch.bfloat16, (T, io.n_q, d), dev)
+        n_q = q.shape[1]
+        qp, qs = _rows(q, "q", k.dtype, (T, n_q, d), dev)
+        op, os_ = _rows(q_out, "q_out", torch.bfloat16, (T, n_q, d), dev)
+    io = MkAppendIo(qp, kp, vp, op, qs, ks, vs, os_, n_q, MK_F32 if k.dtype is torch.float32 else MK_BF16)
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     st = _status(status, dev)
     _call(_lib().mk_kv_append, dev, stream, cache.handle, layer, tok, io, st)
@@ -186,7 +184,6 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
 
 def tree_attn_workspace_bytes(cache: KvCache) -> int:
     """mk_tree_attn_workspace_bytes on the cache's device."""
-    import torch
     with torch.cuda.device(cache.device):
         return int(_lib().mk_tree_attn_workspace_bytes(cache.handle))
 
@@ -197,20 +194,18 @@ def tree_attn(cache: KvCache, layer: int, q, out, cu_seqlens, cache_lens, block_
     """mk_tree_attn: q and out bf16 [tokens][n_q][head_dim]; tree_mask int64
     [tokens][words] (the bits of uint64 words) or None for a run of tokens;
     lse fp32 [tokens][n_q] or None; workspace uint8."""
-    import torch
     dev, bf = cache.device, torch.bfloat16
     if q.dim() != 3:
         _bad(f"q: [tokens][heads][head_dim] is wanted, got {tuple(q.shape)}")
-    T, n_q, d = q.shape
-    io = MkAttnIo(n_q=n_q, window=window, scale=0.0 if scale is None else scale)
+    T, n_q, _ = q.shape
     if scale is not None and not scale > 0:
         _bad(f"scale must be positive, got {scale}")
-    io.q, io.q_stride = _rows(q, "q", bf, (T, n_q, cache.head_dim), dev)
-    io.out, io.out_stride = _rows(out, "out", bf, (T, n_q, cache.head_dim), dev)
-    io.lse = _take(lse, "lse", torch.float32, (T, n_q), dev)
-    if tree_mask is not None:
-        io.mask_words = tree_mask.shape[-1]
-        io.tree_mask = _take(tree_mask, "tree_mask", torch.int64, (T, io.mask_words), dev)
+    qp, qs = _rows(q, "q", bf, (T, n_q, cache.head_dim), dev)
+    op, os_ = _rows(out, "out", bf, (T, n_q, cache.head_dim), dev)
+    words = 0 if tree_mask is None else tree_mask.shape[-1]
+    io = MkAttnIo(qp, op, _take(lse, "lse", torch.float32, (T, n_q), dev),
+                  _take(tree_mask, "tree_mask", torch.int64, (T, words), dev), qs, os_, n_q, words, window,
+                  0.0 if scale is None else scale)
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     ws = _take(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     st = _status(status, dev)
@@ -220,7 +215,6 @@ def tree_attn(cache: KvCache, layer: int, q, out, cu_seqlens, cache_lens, block_
 def kv_commit(cache: KvCache, cache_lens, path, path_lens, block_tables, new_lens=None, status=None,
               stream=None) -> None:
     """mk_kv_commit: path int32 [batch][max_path], path_lens int32 [batch]."""
-    import torch
     dev, i32 = cache.device, torch.int32
     B, width, pages = cache_lens.shape[0], path.shape[-1], block_tables.shape[-1]
     args = (_take(cache_lens, "cache_lens", i32, (B,), dev), _take(path, "path", i32, (B, width), dev),
@@ -240,7 +234,7 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, 
     """mk_beam_select: logits fp32 [requests * beams][vocab] (rows may be
     strided), scores fp32 [requests][beams], finished uint8 [requests][beams];
     outputs [requests][n_out] fp32, int32, int32."""
-    import torch
+    _lib()
     dev, f32, i32 = logits.device, torch.float32, torch.int32
     if scores.dim() != 2 or logits.dim() != 2 or out_scores.dim() != 2:
         _bad("logits, scores and outputs have two dimensions")
@@ -259,7 +253,6 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, 
 def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=None, stream=None) -> None:
     """mk_beam_reorder: lens int32 [requests], parents int32
     [requests][beams], tables int32 [requests * beams][max_pages]."""
-    import torch
     dev, i32 = cache.device, torch.int32
     if parents.dim() != 2:
         _bad(f"parents: [requests][beams] is wanted, got {tuple(parents.shape)}")
@@ -273,5 +266,6 @@ def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=No
 def check_status(status, stream=None) -> None:
     """mk_check_status: waits for the stream; raises MkError if a call that
     was given `status` found a value out of range or gave up a wait."""
+    _lib()
     st = _status(status, status.device)
     _call(_lib().mk_check_status, status.device, stream, st)
