@@ -6,9 +6,9 @@
 // head) pair of the K/V head, in the order token * group + head, so that the
 // rows of a tree share each K/V tile that is read.  All tiles, in the order
 // (sequence, head, query group, tile), are dealt to the SMs in runs of equal
-// cost: a unit for each tile, and for the opening of each item (all tiles of
-// one query group) what the fill and the drain of the pipeline and the output
-// cost (see opening_of).  So a long
+// cost: a unit for each tile, and three for the opening of each item (all tiles
+// of one query group): the fill and the drain of the pipeline and the output
+// cost about as much.  So a long
 // context is split over many SMs, a short one costs no more than it holds, and
 // nothing about the lengths is known to the host.  Where an item is cut by the
 // border between two SMs, each leaves its part (row maxima, sums, unnormalised
@@ -62,7 +62,7 @@ constexpr int kTile = 128;               // slots of a K/V tile, rows of an MMA
 constexpr int kPiece = kTile / 2;        // slots of a piece of S
 constexpr int kRows = 2 * kTile;         // query rows of an item
 constexpr int kThreads = 384;
-constexpr int kOpenOne = 3, kOpenBoth = 1;  // see opening_of
+constexpr int kOpening = 3;              // units before an item's first tile
 constexpr int kMaxItems = 8;             // items planned at a time
 constexpr float kSlack = 8.0f;           // log2: how far the maximum in use may lag
 constexpr int64_t kWaitNs = 2000000000;  // a wait that takes longer is given up
@@ -127,27 +127,19 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Seq& s, int m,
   }
 }
 
-// Units before the first tile of query group m: what a further item costs an
-// SM beside its tiles, about 4 us, in tiles of 1.2 us (up to 128 rows, bound by
-// memory) or 2 us.  None where every SM has a tile at most: an item is one
-// SM's first anyway.
-__device__ __forceinline__ int opening_of(const AttnArgs& a, const Seq& s, int m, bool many) {
-  return !many ? 0 : s.n * a.group - m * kRows > kTile ? kOpenBoth : kOpenOne;
-}
-
 __device__ __forceinline__ int groups_of(const AttnArgs& a, const Seq& s) {
   return (s.n * a.group - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
 
-// Tiles of one K/V head of a sequence, and the units of their openings.
-__device__ __forceinline__ void units_of(const AttnArgs& a, const Seq& s, int64_t& tiles, int64_t& open) {
-  tiles = open = 0;
+// Tiles of one K/V head of a sequence.
+__device__ __forceinline__ int64_t tiles_in(const AttnArgs& a, const Seq& s) {
+  int64_t u = 0;
   for (int m = 0, M = groups_of(a, s); m < M; ++m) {
     int lo, hi;
     tiles_of(a, s, m, lo, hi);
-    tiles += hi - lo;
-    open += opening_of(a, s, m, true);
+    u += hi - lo;
   }
+  return u;
 }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
@@ -162,37 +154,41 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of numbers
   return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// A lane's sequence of a round of 32, and the units of one of its heads.
+// A lane's sequence of a round of 32, and the tiles of one of its heads.
 struct Load {
   Seq s;
-  int64_t tiles, open;
+  int64_t tiles;
 };
 __device__ __forceinline__ Load load_of(const AttnArgs& a, int b) {
-  Load x = {{0, 0, 0}, 0, 0};
+  Load x = {{0, 0, 0}, 0};
   if (b < a.b.batch) {
     x.s = attn_seq(a, b);
-    units_of(a, x.s, x.tiles, x.open);
+    x.tiles = tiles_in(a, x.s);
   }
   return x;
 }
 
-// All units (by one warp), whether they count openings, and the lane's
-// sequence of the first round.
-__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int grid, Load& first, bool& many) {
+// All units (by one warp), the units of an opening, and the lane's sequence of
+// the first round.  Openings cost nothing where every SM has a tile at most:
+// an item is then the first of its SMs.  With more, counting 3 for one took
+// 30 ragged prompts of up to 273 tokens (each over up to 785 slots) from 195
+// to 121 us, 32 trees of 16 tokens over up to 32K slots from 197 to 191 us; 1,
+// 2 and 4 were slower.
+__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int grid, Load& first, int& opening) {
   const int lane = threadIdx.x % 32;
   first = load_of(a, lane);
-  int64_t u = first.tiles, v = first.open;
+  int64_t u = first.tiles, items = groups_of(a, first.s);
   for (int b = lane + 32; b < a.b.batch; b += 32) {
     const Load x = load_of(a, b);
     u += x.tiles;
-    v += x.open;
+    items += groups_of(a, x.s);
   }
   for (int o = 16; o > 0; o >>= 1) {
     u += __shfl_xor_sync(FULL, u, o);
-    v += __shfl_xor_sync(FULL, v, o);
+    items += __shfl_xor_sync(FULL, items, o);
   }
-  many = u * a.pools.n_kv > grid;
-  return (u + (many ? v : 0)) * a.pools.n_kv;
+  opening = u * a.pools.n_kv > grid ? kOpening : 0;
+  return (u + items * opening) * a.pools.n_kv;
 }
 
 // The first unit of CTA c: even runs, the longer ones first.
@@ -223,13 +219,13 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
 // units [u, end), in order, while it returns true.  By one warp, whose lanes hold the first
 // round's sequences; f runs on every lane.
 template <typename F>
-__device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, bool many, int64_t u, int64_t end, F f) {
+__device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, int opening, int64_t u, int64_t end, F f) {
   const int lane = threadIdx.x % 32;
   int64_t base = 0;  // units before this round of sequences
   for (int b0 = 0; b0 < a.b.batch && base < end; b0 += 32) {
     const Load x = b0 == 0 ? first : load_of(a, b0 + lane);
     const Seq s = x.s;
-    const int64_t per_head = x.tiles + (many ? x.open : 0);
+    const int64_t per_head = x.tiles + groups_of(a, s) * opening;
     const int64_t incl = warp_scan(per_head * a.pools.n_kv);
     uint32_t hit = __ballot_sync(FULL, per_head > 0 && base + incl > u && base + incl - per_head * a.pools.n_kv < end);
     while (hit) {
@@ -245,7 +241,7 @@ __device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, 
         for (int m = 0; m < M; ++m) {
           int lo, hi;
           tiles_of(a, q, m, lo, hi);
-          at += opening_of(a, q, m, many);
+          at += opening;
           if (at + (hi - lo) > u) {
             if (at >= end) return;
             if (!f(make_item(a, q, b0 + src, h, m), at)) return;
@@ -899,11 +895,11 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
 }
 
 // The next items of a CTA's units [u, end), which began at `begin` (by one warp).
-__device__ __forceinline__ void plan_items(const AttnArgs& a, Ctl& c, const Load& first, bool many, int64_t begin, int64_t u, int64_t end) {
+__device__ __forceinline__ void plan_items(const AttnArgs& a, Ctl& c, const Load& first, int opening, int64_t begin, int64_t u, int64_t end) {
   const bool one = threadIdx.x % 32 == 0;
   int n = 0;
   int64_t next = end;
-  each_item(a, first, many, u, end, [&](Item it, int64_t at) {
+  each_item(a, first, opening, u, end, [&](Item it, int64_t at) {
     if (one && u == begin && n == 0) {
       a.borders[blockIdx.x].at = at;
       a.borders[blockIdx.x].item = it;
@@ -950,10 +946,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     return;
   }
   Load load;
-  bool many = false;
+  int opening = 0;
   int64_t u = 0, end = 0;
   if (warp == 0) {  // this CTA's units, and its first items
-    const int64_t total = total_units(a, gridDim.x, load, many);
+    const int64_t total = total_units(a, gridDim.x, load, opening);
     u = border(total, blockIdx.x, gridDim.x);
     end = border(total, blockIdx.x + 1, gridDim.x);
     if (tid == 0) {
@@ -963,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       a.borders[blockIdx.x].at = u;  // until the plan says more
       if (blockIdx.x == 0) a.borders[gridDim.x].first = total;
     }
-    plan_items(a, c, load, many, u, u, end);
+    plan_items(a, c, load, opening, u, u, end);
   } else if (warp == 1) {
     if (tid == 32) {
       c.abort = 0;
@@ -1003,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     MmaState mma;
     while (u < end && ok) {
       if (u > begin) {
-        if (warp == 0) plan_items(a, c, load, many, begin, u, end);
+        if (warp == 0) plan_items(a, c, load, opening, begin, u, end);
         __syncthreads();
       }
       if (warp == 0)
