@@ -33,6 +33,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t o) {
   return o == 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
+// The largest number below the one ordered as o (-0 has no code of its own).
+__device__ __forceinline__ float just_below(uint32_t o) { return unordered(o - (o == 0x80000000u ? 2 : 1)); }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return (uint64_t)ordered(x) << 32 | (uint32_t)~index; }
 
 struct Key2 {  // a score in 64 bits and the candidate's index
@@ -71,99 +73,127 @@ __device__ __forceinline__ float ex2(float x) {
 // e^d for d <= 0: the error is |d| 2^-23 + 2^-22, least where the term counts most.
 __device__ __forceinline__ float e_to(float d) { return ex2(d * 1.44269504089f); }
 
-// A warp's best candidates so far.  A tile's logits are compared with the n-th
-// best as numbers; only a tile that beats it looks further, so the stream
-// costs the maximum and the exponentials.
+// A warp's candidates: at least the n best of its logits so far.  A tile's
+// logits are compared with a bound as numbers; only lanes that beat it look
+// further, so the stream costs the maximum and the exponentials.
 template <int N>  // n_out is at most N
-struct Best {
-  static constexpr int kGroups = N / 32;               // of a lane's logits in a tile
-  static constexpr int kFull = 2 * N;                  // kept before they are sorted out
-  uint64_t buf[kFull + kWarpTile];
+struct alignas(16) Best {
+  static constexpr int kGroups = N / 32;  // of a lane's logits in a tile
+  static constexpr int kFull = 2 * N;     // kept before they are sorted out
+  uint64_t buf[kFull + kWarpTile + 8];    // eight zeros behind the last
   uint64_t next[N];
+  int count;
+};
+template <int N>
+struct Parts {
+  Best<N> best[kWarps];
+  uint64_t list[kWarps * Best<N>::kFull + 8];
+  int count;
+  uint32_t bound;  // the best of the warps' bounds, ordered
 };
 
-// The n best of buf[0 .. count), best first; returns how many there are.
+// How many of keys[0 .. count) are above `mine`; eight zeros follow the last.
+__device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t mine) {
+  int rank = 0;
+  for (int j = 0; j < count; j += 8) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) rank += keys[j + x] > mine;
+  }
+  return rank;
+}
+
+// Leaves the n best of buf[0 .. count), best first; returns how many there are.
 template <int N>
 __device__ __forceinline__ int sort_out(Best<N>& k, int count, int n) {
   const int lane = threadIdx.x % 32;
+  if (lane < 8) k.buf[count + lane] = 0;
   __syncwarp();
   for (int i = lane; i < count; i += 32) {
     const uint64_t mine = k.buf[i];
-    int rank = 0;
-    for (int j = 0; j < count; ++j) rank += k.buf[j] > mine;
+    const int rank = rank_in(k.buf, count, mine);
     if (rank < n) k.next[rank] = mine;
   }
   __syncwarp();
   const int m = min(count, n);
   for (int i = lane; i < m; i += 32) k.buf[i] = k.next[i];
   __syncwarp();
+  if (lane == 0) k.count = m;
+  __syncwarp();
   return m;
 }
 
-// The n-th best of the maxima of the tile's 32 kGroups groups, 0 if fewer hold
-// a logit: at least n of the tile's keys reach it.
+// The n-th largest of the maxima of a tile's 32 kGroups groups, ordered: at
+// least n of the tile's logits reach it.
 template <int N>
-__device__ __forceinline__ uint64_t bound_of(Best<N>& k, const uint64_t (&key)[kPer], int n) {
+__device__ __forceinline__ uint32_t bound_of(Best<N>& k, const float (&v)[kPer], int n) {
   constexpr int G = Best<N>::kGroups;
   const int lane = threadIdx.x % 32;
-  uint64_t top[G], found = 0;
-  int rank[G];
-  __syncwarp();
+  float* all = reinterpret_cast<float*>(k.next);
+  float top[G];
+  int above[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    top[g] = 0;
+    top[g] = v[g * (kPer / G)];
 #pragma unroll
-    for (int i = 0; i < kPer / G; ++i) top[g] = max(top[g], key[g * (kPer / G) + i]);
-    k.next[g * 32 + lane] = top[g];
+    for (int i = 1; i < kPer / G; ++i) top[g] = fmaxf(top[g], v[g * (kPer / G) + i]);
+    all[g * 32 + lane] = top[g];
+    above[g] = 0;
   }
   __syncwarp();
+#pragma unroll 8
+  for (int j = 0; j < 8 * G; ++j) {
+    const float4 o = reinterpret_cast<const float4*>(all)[j];
 #pragma unroll
-  for (int g = 0; g < G; ++g) rank[g] = 0;
-#pragma unroll 4
-  for (int j = 0; j < 32 * G; ++j) {
-    const uint64_t other = k.next[j];
-#pragma unroll
-    for (int g = 0; g < G; ++g) rank[g] += other > top[g];
+    for (int g = 0; g < G; ++g) above[g] += (o.x > top[g]) + (o.y > top[g]) + (o.z > top[g]) + (o.w > top[g]);
   }
+  uint32_t least = 0xffffffffu;
 #pragma unroll
   for (int g = 0; g < G; ++g)
-    if (rank[g] == n - 1) found = top[g];
-  const uint32_t who = __ballot_sync(FULL, found != 0);
-  return who ? __shfl_sync(FULL, found, __ffs(who) - 1) : 0;
+    if (above[g] < n) least = min(least, ordered(top[g]));
+  return __reduce_min_sync(FULL, least);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) select_parts(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint4 raw[];
-  Best<N>* best = reinterpret_cast<Best<N>*>(raw);
-  __shared__ int counts[kWarps];
+  Parts<N>& sh = *reinterpret_cast<Parts<N>*>(raw);
   __shared__ float wm[kWarps];
   __shared__ double ws[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = a.n_out;
-  if (a.finished && a.finished[row]) return;
   const int lo = part * a.part_len, hi = min(a.vocab, lo + a.part_len);
   const float* x = a.logits + row * a.stride;
-  Best<N>& k = best[warp];
-  int count = 0;
-  uint64_t tau = 0;  // the n-th best key, 0 until there are n
-  float tau_f = 0.0f;
-  float m = -INFINITY, s = 0.0f;
-  for (int base = lo; base < hi; base += kTile) {
-    // four runs of four per thread
-    float v[kPer];
+  // four runs of four per thread
+  float next[kPer];
+  auto load = [&](int base) {
     const bool whole = a.vec && base + kTile <= hi;
 #pragma unroll
     for (int q = 0; q < kPer / 4; ++q) {
       const int at = base + (q * kThreads + tid) * 4;
       if (whole) {
         const float4 f = __ldcs(reinterpret_cast<const float4*>(x + at));
-        v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+        next[4 * q] = f.x, next[4 * q + 1] = f.y, next[4 * q + 2] = f.z, next[4 * q + 3] = f.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * q + j] = at + j < hi ? x[at + j] : -INFINITY;
+        for (int j = 0; j < 4; ++j) next[4 * q + j] = at + j < hi ? x[at + j] : -INFINITY;
       }
     }
+  };
+  if (a.finished && a.finished[row]) return;
+  load(lo);
+  Best<N>& k = sh.best[warp];
+  if (lane == 0) k.count = 0;
+  if (tid == 0) sh.bound = 0, sh.count = 0;
+  __syncthreads();
+  int count = 0;
+  bool bounded = false;
+  float tau = -INFINITY;  // at least n of the warp's logits reach it, once bounded
+  float m = -INFINITY, s = 0.0f;
+  for (int base = lo; base < hi; base += kTile) {
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = next[i];
+    if (base + kTile < hi) load(base + kTile);
     float t = v[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) t = fmaxf(t, v[i]);
@@ -176,61 +206,65 @@ __global__ void __launch_bounds__(kThreads, 4) select_parts(const __grid_constan
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) s0 += e_to(v[i] - z), s1 += e_to(v[i + 1] - z);
     s += s0 + s1;
-    // Equal logits of later tiles have higher indices: only a larger one passes.
-    if (!__any_sync(FULL, tau == 0 || t > tau_f)) continue;
-    uint64_t key[kPer];
-    int pass = 0;
+    // Equal logits of the warp's later tiles have higher indices: only a larger
+    // one than its own bound passes.  Another warp's bound may stand at a
+    // higher index: an equal one passes.
+    float least = tau;
+    bool all = false;
+    if (bounded) {
+      const uint32_t shared = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
+      if (shared > ordered(-INFINITY)) least = fmaxf(least, just_below(shared));
+      if (!__any_sync(FULL, t > least)) continue;
+    } else {  // the first tile, or the first with n logits
+      const uint32_t o = bound_of(k, v, n);
+      all = o <= ordered(-INFINITY);  // too few numbers: every logit in the range
+      bounded = !all;
+      if (bounded) tau = unordered(o), least = just_below(o);
+    }
+    if (all || t > least) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = base + (i / 4 * kThreads + tid) * 4 + i % 4;
-      key[i] = at < hi ? key_of(v[i], at) : 0;
-      pass += key[i] > tau;
-    }
-    uint64_t above = tau;
-    if (__reduce_add_sync(FULL, pass) > N) {  // many: the tile's own n-th best may be nearer
-      const uint64_t bound = bound_of(k, key, n);
-      if (bound > above) above = bound - 1;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t in = __ballot_sync(FULL, key[i] > above);
-      if (key[i] > above) k.buf[count + __popc(in & ((1u << lane) - 1))] = key[i];
-      count += __popc(in);
-    }
-    if (count > Best<N>::kFull || (tau == 0 && count >= n)) {
-      count = sort_out(k, count, n);
-      if (count == n) {
-        tau = k.buf[n - 1];
-        tau_f = unordered((uint32_t)(tau >> 32));
+      for (int i = 0; i < kPer; ++i) {
+        const int at = base + (i / 4 * kThreads + tid) * 4 + i % 4;
+        if (all ? at < hi : v[i] > least) k.buf[atomicAdd(&k.count, 1)] = key_of(v[i], at);
       }
     }
+    __syncwarp();
+    count = *reinterpret_cast<volatile int*>(&k.count);
+    if (count > Best<N>::kFull || (!bounded && count >= n)) {
+      count = sort_out(k, count, n);
+      tau = unordered((uint32_t)(k.buf[n - 1] >> 32));
+      bounded = tau == tau;  // not NaN
+    }
+    if (bounded && lane == 0) atomicMax(&sh.bound, ordered(tau));
   }
-  count = sort_out(k, count, n);
   // the sums of the threads, joined in 64 bits
   float bm = m;
   for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(FULL, bm, o));
-  if (lane == 0) wm[warp] = bm, counts[warp] = count;
+  if (lane == 0) wm[warp] = bm;
   __syncthreads();
   bm = wm[0];
   for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, wm[w]);
   // s times e^(m - bm): the factor's error, an fp32 exponential's, is that of the terms themselves
-  double d = m == -INFINITY ? (double)s : (double)s * (double)e_to(m - bm);
+  double d = m == -INFINITY ? (double)s : (double)(s * e_to(m - bm));
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(FULL, d, o);
   if (lane == 0) ws[warp] = d;
-  // the n best of the warps' candidates
-  uint64_t* out = a.keys + ((int64_t)row * a.parts + part) * n;
-  int all = 0;
-  for (int w = 0; w < kWarps; ++w) all += counts[w];
+  // the n best of the warps' candidates; none below the bound is among them
   for (int i = lane; i < count; i += 32) {
     const uint64_t mine = k.buf[i];
-    int rank = 0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int j = 0; j < counts[w]; ++j) rank += best[w].buf[j] > mine;
+    if ((uint32_t)(mine >> 32) >= sh.bound) sh.list[atomicAdd(&sh.count, 1)] = mine;
+  }
+  __syncthreads();
+  const int c = sh.count;
+  if (tid < 8) sh.list[c + tid] = 0;
+  __syncthreads();
+  uint64_t* out = a.keys + ((int64_t)row * a.parts + part) * n;
+  for (int i = tid; i < c; i += kThreads) {
+    const uint64_t mine = sh.list[i];
+    const int rank = rank_in(sh.list, c, mine);
     if (rank < n) out[rank] = mine;
   }
   for (int i = tid; i < n; i += kThreads)
-    if (i >= all) out[i] = 0;
-  __syncthreads();
+    if (i >= c) out[i] = 0;
   if (tid == 0) {
     d = 0;
     for (int w = 0; w < kWarps; ++w) d += ws[w];
@@ -241,29 +275,40 @@ __global__ void __launch_bounds__(kThreads, 4) select_parts(const __grid_constan
 constexpr int kMaxBeams = 64;
 constexpr int kDirect = 384;  // candidates that are ranked against each other at once
 
-// The request's candidates, and its best so far.
+// The request's candidates, and its best so far; scores and indices apart, so
+// that a comparison is two plain loads.
 struct Joined {
-  Key2 buf[kMaxOut * kPer + kMaxOut];
+  static constexpr int kRoom = kMaxOut * kPer + kMaxOut;
+  uint64_t score[kRoom + 8];
+  uint32_t index[kRoom + 8];
   Key2 next[kMaxOut];
   Key2 best[kThreads];
   Key2 tau, bound;
   int count;
 };
 
-// Leaves the n best of buf[0 .. count), best first, in buf and sets tau.
+// Leaves the n best of the candidates, best first, and sets tau.
 __device__ __forceinline__ void sort_out(Joined& k, int n) {
   __syncthreads();
-  const int c = k.count;
-  for (int i = threadIdx.x; i < c; i += kThreads) {
-    const Key2 mine = k.buf[i];
+  const int c = k.count, tid = threadIdx.x;
+  if (tid < 8) k.score[c + tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < c; i += kThreads) {
+    const Key2 mine = {k.score[i], k.index[i]};
     int rank = 0;
-    for (int j = 0; j < c; ++j) rank += above(k.buf[j], mine);
+    for (int j = 0; j < c; j += 8) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint64_t s = k.score[j + x];
+        rank += (s > mine.score) | ((s == mine.score) & (k.index[j + x] > mine.index));
+      }
+    }
     if (rank < n) k.next[rank] = mine;
   }
   __syncthreads();
   const int m = min(c, n);
-  for (int i = threadIdx.x; i < m; i += kThreads) k.buf[i] = k.next[i];
-  if (threadIdx.x == 0) {
+  for (int i = tid; i < m; i += kThreads) k.score[i] = k.next[i].score, k.index[i] = k.next[i].index;
+  if (tid == 0) {
     k.count = m;
     if (m == n) k.tau = k.next[n - 1];
   }
@@ -273,41 +318,51 @@ __device__ __forceinline__ void sort_out(Joined& k, int n) {
 __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint4 raw[];
   Joined& k = *reinterpret_cast<Joined*>(raw);
-  __shared__ double top[kMaxBeams];
   __shared__ double lse[kMaxBeams];  // NaN: every score of the beam is -inf
   __shared__ double share[kMaxBeams * kMaxParts];
+  __shared__ float top[kMaxBeams], scores[kMaxBeams];
   __shared__ bool done[kMaxBeams];
-  const int r = blockIdx.x, tid = threadIdx.x, W = a.beams, n = a.n_out;
+  const int r = blockIdx.x, tid = threadIdx.x, W = a.beams, n = a.n_out, parts = a.parts;
+  const int per_row = parts * n, N = W * per_row;
   if (tid == 0) {
     k.count = 0;
     k.tau = {0, 0};
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the parts' sums, joined in 64 bits: a thread per part, then per beam
-  const double2* sums = a.sums + (int64_t)r * W * a.parts;
   for (int w = tid; w < W; w += kThreads) {
     done[w] = a.finished && a.finished[r * W + w];
-    top[w] = -INFINITY;
-    if (!done[w])
-      for (int i = 0; i < a.parts; ++i) top[w] = fmax(top[w], sums[w * a.parts + i].x);
+    scores[w] = a.scores[r * W + w];
   }
-  __syncthreads();
-  for (int i = tid; i < W * a.parts; i += kThreads) {
-    const int w = i / a.parts;
-    if (done[w]) continue;
-    const double2 p = sums[i];
-    share[i] = p.x == top[w] || p.y == 0.0 ? p.y : p.y * exp(p.x - top[w]);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first candidates on their way beside the parts' sums
+  const uint64_t* keys = a.keys + (int64_t)r * N;
+  const uint64_t early = tid < N ? keys[tid] : 0;
+  // the parts' sums, joined in 64 bits: a thread per part, then per beam (the
+  // logarithm's hundred or so 64-bit operations are most of this kernel's time)
+  const double2* sums = a.sums + (int64_t)r * W * parts;
+  for (int i0 = 0; i0 < W * parts; i0 += kThreads) {
+    const int i = i0 + tid, w = i / parts;
+    const bool in = i < W * parts;
+    double2 p = make_double2(0, 0);
+    if (in) p = sums[i];
+    __syncthreads();  // done[] of this block, and top[] of the round before
+    if (in && done[w]) p = make_double2(0, 0);
+    if (in && i % parts == 0) {
+      float t = (float)p.x;  // an fp32 number
+      for (int x = 1; x < parts; ++x) t = fmaxf(t, done[w] ? 0.0f : (float)sums[i + x].x);
+      top[w] = t;
+    }
+    __syncthreads();
+    if (in) share[i] = (float)p.x == top[w] || p.y == 0.0 ? p.y : p.y * exp(p.x - (double)top[w]);
   }
   __syncthreads();
   for (int w = tid; w < W; w += kThreads) {
     if (done[w]) continue;
     double sum = 0;
-    for (int i = 0; i < a.parts; ++i) sum += share[w * a.parts + i];
-    const double l = top[w] + log(sum);
-    lse[w] = isfinite(l) && a.scores[r * W + w] > -INFINITY ? l : NAN;
+    for (int i = 0; i < parts; ++i) sum += share[w * parts + i];
+    const double l = (double)top[w] + log(sum);
+    lse[w] = isfinite(l) && scores[w] > -INFINITY ? l : NAN;
   }
   __syncthreads();
-  const int per_row = a.parts * n, N = W * per_row;
   for (int base = 0; base < N; base += kTile) {
     Key2 key[kPer], b = {0, 0};
 #pragma unroll
@@ -315,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       const int c = base + i * kThreads + tid;
       key[i] = {0, 0};
       if (c >= N) continue;
-      const int w = c / per_row, j = c % per_row, row = r * W + w;
-      const double cum = a.scores[row];
+      const int w = c / per_row, j = c % per_row;
+      const double cum = scores[w];
       double score = -INFINITY;
       int token;
       if (done[w]) {
@@ -328,7 +383,7 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
         token = j;
         if (j >= n || token >= a.vocab) continue;
       } else {
-        const uint64_t q = a.keys[(int64_t)row * per_row + j];
+        const uint64_t q = base == 0 && i == 0 ? early : keys[c];
         if (q == 0) continue;
         token = (int)~(uint32_t)q;
         score = cum + ((double)unordered((uint32_t)(q >> 32)) - lse[w]);
@@ -345,7 +400,11 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       if (tid == 0) k.bound = bound;
       __syncthreads();
       int rank = 0;
-      for (int j = 0; j < kThreads; ++j) rank += above(k.best[j], b);
+#pragma unroll 8
+      for (int j = 0; j < kThreads; ++j) {
+        const Key2 o = k.best[j];
+        rank += (o.score > b.score) | ((o.score == b.score) & (o.index > b.index));
+      }
       if (rank == n - 1 && b.score != 0 && above(b, bound)) k.bound = b;
       __syncthreads();
       bound = k.bound;
@@ -353,13 +412,17 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
     const bool raised = above(bound, k.tau);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (raised ? !above(bound, key[i]) : above(key[i], bound)) k.buf[atomicAdd(&k.count, 1)] = key[i];
+      if (raised ? !above(bound, key[i]) : above(key[i], bound)) {
+        const int at = atomicAdd(&k.count, 1);
+        k.score[at] = key[i].score;
+        k.index[at] = key[i].index;
+      }
     sort_out(k, n);
   }
   for (int i = tid; i < n; i += kThreads) {
-    const uint32_t c = ~k.buf[i].index;
+    const uint32_t c = ~k.index[i];
     const int64_t o = (int64_t)r * n + i;
-    a.out_scores[o] = (float)unordered64(k.buf[i].score);
+    a.out_scores[o] = (float)unordered64(k.score[i]);
     a.out_parents[o] = (int32_t)(c / (uint32_t)a.vocab);
     a.out_tokens[o] = (int32_t)(c % (uint32_t)a.vocab);
   }
@@ -436,9 +499,9 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
   if (rc != MK_OK) return rc;
   const dim3 grid((unsigned)a.parts, (unsigned)rows);
   if (n_out <= 32) {
-    select_parts<32><<<grid, kThreads, kWarps * sizeof(Best<32>), st>>>(a);
+    select_parts<32><<<grid, kThreads, sizeof(Parts<32>), st>>>(a);
   } else {
-    constexpr int wide = (int)(kWarps * sizeof(Best<kMaxOut>));
+    constexpr int wide = (int)sizeof(Parts<kMaxOut>);
     rc = allow_smem(wide_ready, reinterpret_cast<const void*>(&select_parts<kMaxOut>), wide, "select");
     if (rc != MK_OK) return rc;
     select_parts<kMaxOut><<<grid, kThreads, wide, st>>>(a);
