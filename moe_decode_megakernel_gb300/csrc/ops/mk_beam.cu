@@ -78,9 +78,8 @@ __device__ __forceinline__ float e_to(float d) { return ex2(d * 1.44269504089f);
 // further, so the stream costs the maximum and the exponentials.
 template <int N>  // n_out is at most N
 struct alignas(16) Best {
-  static constexpr int kGroups = N / 32;  // of a lane's logits in a tile
-  static constexpr int kFull = 2 * N;     // kept before they are sorted out
-  uint64_t buf[kFull + kWarpTile + 8];    // eight zeros behind the last
+  static constexpr int kFull = 2 * N;   // kept before they are sorted out
+  uint64_t buf[kFull + kWarpTile + 8];  // eight zeros behind the last
   uint64_t next[N];
   int count;
 };
@@ -88,8 +87,10 @@ template <int N>
 struct Parts {
   Best<N> best[kWarps];
   uint64_t list[kWarps * Best<N>::kFull + 8];
+  float top[kThreads];  // the first tile's maxima of each thread
   int count;
-  uint32_t bound;  // the best of the warps' bounds, ordered
+  uint32_t least;  // the n-th largest of them, ordered
+  uint32_t bound;  // the best bound of any warp, ordered
 };
 
 // How many of keys[0 .. count) are above `mine`; eight zeros follow the last.
@@ -122,35 +123,23 @@ __device__ __forceinline__ int sort_out(Best<N>& k, int count, int n) {
   return m;
 }
 
-// The n-th largest of the maxima of a tile's 32 kGroups groups, ordered: at
-// least n of the tile's logits reach it.
+// The n-th largest of the threads' maxima of a tile, ordered: at least n of the
+// tile's logits reach it, and of 4096 random ones few more than n do (the
+// n-th best of a warp's 512 lets eight times as many pass).
 template <int N>
-__device__ __forceinline__ uint32_t bound_of(Best<N>& k, const float (&v)[kPer], int n) {
-  constexpr int G = Best<N>::kGroups;
-  const int lane = threadIdx.x % 32;
-  float* all = reinterpret_cast<float*>(k.next);
-  float top[G];
-  int above[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    top[g] = v[g * (kPer / G)];
-#pragma unroll
-    for (int i = 1; i < kPer / G; ++i) top[g] = fmaxf(top[g], v[g * (kPer / G) + i]);
-    all[g * 32 + lane] = top[g];
-    above[g] = 0;
-  }
-  __syncwarp();
+__device__ __forceinline__ uint32_t bound_of(Parts<N>& sh, float t, int n) {
+  sh.top[threadIdx.x] = t;
+  __syncthreads();
+  int above = 0;
 #pragma unroll 8
-  for (int j = 0; j < 8 * G; ++j) {
-    const float4 o = reinterpret_cast<const float4*>(all)[j];
-#pragma unroll
-    for (int g = 0; g < G; ++g) above[g] += (o.x > top[g]) + (o.y > top[g]) + (o.z > top[g]) + (o.w > top[g]);
+  for (int j = 0; j < kThreads / 4; ++j) {
+    const float4 o = reinterpret_cast<const float4*>(sh.top)[j];
+    above += (o.x > t) + (o.y > t) + (o.z > t) + (o.w > t);
   }
-  uint32_t least = 0xffffffffu;
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-    if (above[g] < n) least = min(least, ordered(top[g]));
-  return __reduce_min_sync(FULL, least);
+  const uint32_t least = __reduce_min_sync(FULL, above < n ? ordered(t) : 0xffffffffu);
+  if (threadIdx.x % 32 == 0) atomicMin(&sh.least, least);
+  __syncthreads();
+  return sh.least;
 }
 
 template <int N>
@@ -183,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
   load(lo);
   Best<N>& k = sh.best[warp];
   if (lane == 0) k.count = 0;
-  if (tid == 0) sh.bound = 0, sh.count = 0;
+  if (tid == 0) sh.bound = 0, sh.count = 0, sh.least = 0xffffffffu;
   __syncthreads();
   int count = 0;
   bool bounded = false;
-  float tau = -INFINITY;  // at least n of the warp's logits reach it, once bounded
+  float tau = -INFINITY;  // at least n logits of this and earlier tiles reach it, once bounded
   float m = -INFINITY, s = 0.0f;
   for (int base = lo; base < hi; base += kTile) {
     float v[kPer];
@@ -206,21 +195,21 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) s0 += e_to(v[i] - z), s1 += e_to(v[i + 1] - z);
     s += s0 + s1;
-    // Equal logits of the warp's later tiles have higher indices: only a larger
-    // one than its own bound passes.  Another warp's bound may stand at a
-    // higher index: an equal one passes.
+    // Equal logits of later tiles have higher indices: only a larger one than the
+    // first tile's bound, or the warp's own, passes.  Another warp's later bound
+    // may stand at a higher index: an equal one passes.
     float least = tau;
     bool all = false;
+    if (base == lo) {
+      const uint32_t o = bound_of(sh, t, n);
+      if (o > ordered(-INFINITY)) bounded = true, tau = unordered(o), least = just_below(o);
+    }
     if (bounded) {
       const uint32_t shared = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
-      if (shared > ordered(-INFINITY)) least = fmaxf(least, just_below(shared));
+      if (base != lo && shared > ordered(-INFINITY)) least = fmaxf(least, just_below(shared));
       if (!__any_sync(FULL, t > least)) continue;
-    } else {  // the first tile, or the first with n logits
-      const uint32_t o = bound_of(k, v, n);
-      all = o <= ordered(-INFINITY);  // too few numbers: every logit in the range
-      bounded = !all;
-      if (bounded) tau = unordered(o), least = just_below(o);
     }
+    all = !bounded;  // too few numbers so far: every logit in the range
     if (all || t > least) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
