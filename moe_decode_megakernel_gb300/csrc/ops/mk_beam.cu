@@ -65,13 +65,9 @@ struct SelectArgs {
   bool vec;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // e^d for d <= 0: the error is |d| 2^-23 + 2^-22, least where the term counts most.
-__device__ __forceinline__ float e_to(float d) { return ex2(d * 1.44269504089f); }
+constexpr float kLog2e = 1.44269504089f;
+__device__ __forceinline__ float e_to(float d) { return ex2(d * kLog2e); }
 
 // A warp's candidates: at least the n best of its logits so far.  A tile's
 // logits are compared with a bound as numbers; only lanes that beat it look
@@ -87,7 +83,7 @@ template <int N>
 struct Parts {
   Best<N> best[kWarps];
   uint64_t list[kWarps * Best<N>::kFull + 8];
-  float top[kThreads];  // the first tile's maxima of each thread
+  float top[kThreads];  // the groups' maxima
   int count;
   uint32_t least;  // the n-th largest of them, ordered
   uint32_t bound;  // the best bound of any warp, ordered
@@ -103,41 +99,59 @@ __device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t
   return rank;
 }
 
-// Leaves the n best of buf[0 .. count), best first; returns how many there are.
+// Leaves the n best of buf[0 .. count), count >= n, in no order, and returns
+// the least of them: the largest K, found bit by bit, that n keys reach.
 template <int N>
-__device__ __forceinline__ int sort_out(Best<N>& k, int count, int n) {
+__device__ __forceinline__ uint64_t keep_best(Best<N>& k, int count, int n) {
   const int lane = threadIdx.x % 32;
-  if (lane < 8) k.buf[count + lane] = 0;
+  uint64_t least = 0;
   __syncwarp();
-  for (int i = lane; i < count; i += 32) {
-    const uint64_t mine = k.buf[i];
-    const int rank = rank_in(k.buf, count, mine);
-    if (rank < n) k.next[rank] = mine;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t t = least | (uint64_t)1 << bit;
+    int reach = 0;
+    for (int i = lane; i < count; i += 32) reach += k.buf[i] >= t;
+    reach = __reduce_add_sync(FULL, reach);
+    if (reach >= n) least = t;
+    if (reach == n) break;
+  }
+  int kept = 0;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const uint64_t mine = i0 + lane < count ? k.buf[i0 + lane] : 0;
+    const uint32_t in = __ballot_sync(FULL, mine >= least);
+    if (mine >= least) k.next[kept + __popc(in & ((1u << lane) - 1))] = mine;
+    kept += __popc(in);
   }
   __syncwarp();
-  const int m = min(count, n);
-  for (int i = lane; i < m; i += 32) k.buf[i] = k.next[i];
+  for (int i = lane; i < n; i += 32) k.buf[i] = k.next[i];
+  if (lane == 0) k.count = n;
   __syncwarp();
-  if (lane == 0) k.count = m;
-  __syncwarp();
-  return m;
+  return least;
 }
 
-// The n-th largest of the threads' maxima of a tile, ordered: at least n of the
-// tile's logits reach it, and of 4096 random ones few more than n do (the
-// n-th best of a warp's 512 lets eight times as many pass).
+// The n-th largest of the maxima of the block's groups of threads, ordered: at
+// least n of the logits seen so far reach it.  64 groups for n_out up to 32,
+// 256 beyond: of 4096 random logits few more than n reach it (the n-th best of
+// a warp's 512 would let eight times as many pass).
 template <int N>
 __device__ __forceinline__ uint32_t bound_of(Parts<N>& sh, float t, int n) {
-  sh.top[threadIdx.x] = t;
+  constexpr int kLanes = N == 32 ? 4 : 1, kGroups = kThreads / kLanes;
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) t = fmaxf(t, __shfl_xor_sync(FULL, t, o));
+  if (tid % kLanes == 0) sh.top[tid / kLanes] = t;
+  if (tid == 0) sh.least = 0xffffffffu;
   __syncthreads();
-  int above = 0;
+  if (tid < kGroups) {
+    const float mine = sh.top[tid];
+    int above = 0;
 #pragma unroll 8
-  for (int j = 0; j < kThreads / 4; ++j) {
-    const float4 o = reinterpret_cast<const float4*>(sh.top)[j];
-    above += (o.x > t) + (o.y > t) + (o.z > t) + (o.w > t);
+    for (int j = 0; j < kGroups / 4; ++j) {
+      const float4 o = reinterpret_cast<const float4*>(sh.top)[j];
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    }
+    const uint32_t least = __reduce_min_sync(FULL, above < n ? ordered(mine) : 0xffffffffu);
+    if (tid % 32 == 0) atomicMin(&sh.least, least);
   }
-  const uint32_t least = __reduce_min_sync(FULL, above < n ? ordered(t) : 0xffffffffu);
-  if (threadIdx.x % 32 == 0) atomicMin(&sh.least, least);
   __syncthreads();
   return sh.least;
 }
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
   load(lo);
   Best<N>& k = sh.best[warp];
   if (lane == 0) k.count = 0;
-  if (tid == 0) sh.bound = 0, sh.count = 0, sh.least = 0xffffffffu;
+  if (tid == 0) sh.bound = 0, sh.count = 0;
   __syncthreads();
   int count = 0;
   bool bounded = false;
@@ -191,22 +205,35 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
       m = t;
     }
     const float z = m == -INFINITY ? 0.0f : m;
-    float s0 = 0.0f, s1 = 0.0f;
+    const uint32_t zb = __float_as_uint(-z), eb = __float_as_uint(kLog2e);
+    uint64_t sums = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) s0 += e_to(v[i] - z), s1 += e_to(v[i + 1] - z);
-    s += s0 + s1;
-    // Equal logits of later tiles have higher indices: only a larger one than the
-    // first tile's bound, or the warp's own, passes.  Another warp's later bound
-    // may stand at a higher index: an equal one passes.
+    for (int i = 0; i < kPer; i += 2) {
+      float2 e = halves(mul2(add2(pair(__float_as_uint(v[i]), __float_as_uint(v[i + 1])), pair(zb, zb)), pair(eb, eb)));
+      e.x = ex2(e.x), e.y = ex2(e.y);
+      sums = add2(sums, pair(__float_as_uint(e.x), __float_as_uint(e.y)));
+    }
+    s += halves(sums).x + halves(sums).y;
+    // A bound of the whole block after 1, 2, 4, 8 ... tiles (of the running
+    // maxima), and each warp's own once its buffer was full.  Equal logits of
+    // later tiles have higher indices: only a larger one passes a bound of
+    // earlier tiles.  This tile's bound, or one of another warp that may be
+    // further on, lets an equal one pass.
     float least = tau;
+    const int tile = (base - lo) / kTile;
     bool all = false;
-    if (base == lo) {
-      const uint32_t o = bound_of(sh, t, n);
-      if (o > ordered(-INFINITY)) bounded = true, tau = unordered(o), least = just_below(o);
+    if ((tile & (tile + 1)) == 0) {
+      const uint32_t o = bound_of(sh, m, n);
+      if (o > ordered(-INFINITY)) {
+        if (tid == 0) atomicMax(&sh.bound, o);
+        least = fmaxf(least, just_below(o));
+        tau = fmaxf(tau, unordered(o));
+        bounded = true;
+      }
     }
     if (bounded) {
       const uint32_t shared = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
-      if (base != lo && shared > ordered(-INFINITY)) least = fmaxf(least, just_below(shared));
+      if (shared > ordered(-INFINITY)) least = fmaxf(least, just_below(shared));
       if (!__any_sync(FULL, t > least)) continue;
     }
     all = !bounded;  // too few numbers so far: every logit in the range
@@ -220,11 +247,14 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
     __syncwarp();
     count = *reinterpret_cast<volatile int*>(&k.count);
     if (count > Best<N>::kFull || (!bounded && count >= n)) {
-      count = sort_out(k, count, n);
-      tau = unordered((uint32_t)(k.buf[n - 1] >> 32));
-      bounded = tau == tau;  // not NaN
+      const uint32_t o = (uint32_t)(keep_best(k, count, n) >> 32);
+      count = n;
+      if (o >= ordered(-INFINITY)) {  // n numbers among them
+        tau = fmaxf(tau, unordered(o));
+        bounded = true;
+        if (lane == 0) atomicMax(&sh.bound, o);
+      }
     }
-    if (bounded && lane == 0) atomicMax(&sh.bound, ordered(tau));
   }
   // the sums of the threads, joined in 64 bits
   float bm = m;

@@ -914,3 +914,21 @@ def test_agrees_with_the_decode_step(workload):
         tol = plain.bf16_bound(ref) + spread * (2.0 ** -8 + 2 * size[:, None] * 2.0 ** -8)
         assert ((out[b].cpu().double() - ref).abs() <= tol).all()
         assert ((attn[b].cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("low", [-math.inf, -1e30, -3.4028234663852886e38])
+def test_select_masked_vocabulary(low):
+    """Constrained decoding: a few tokens allowed, all others at one low value (more of them than any bound keeps out)."""
+    g = gen(46)
+    R, W, V, n = 3, 4, 30000, 16
+    logits = torch.full((R, W, V), low, device=DEV)
+    allowed = torch.randint(V, (R, W, 10), generator=g, device=DEV)
+    logits.scatter_(2, allowed, torch.randn(R, W, 10, generator=g, device=DEV))
+    logits[1] = low  # nothing allowed
+    logits[2, :, 29000:] = torch.randn(W, 1000, generator=g, device=DEV)  # the last tiles alone
+    scores = -torch.rand(R, W, generator=g, device=DEV)
+    got = run_select(logits, scores, n)
+    best, beam, token = plain.select(logits.cpu(), scores.cpu(), n)
+    check_select(got, logits, scores, n)
+    for r in (0, 2):
+        assert torch.equal(got[1][r].cpu().long(), beam[r]) and torch.equal(got[2][r].cpu().long(), token[r])
