@@ -480,17 +480,19 @@ struct MmaState {
 // addresses there (issued by a lone thread an MMA costs 80 cycles, behind a
 // branch of one lane 45, where it runs 32 or 64).  One elected lane issues.
 // One warp for both groups would spend on barriers and issue what the MMAs of
-// a step take.
+// a step take; for the same reason the steps are written out two by two.
 template <int D>
 __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl& c, MmaState& st, const int w) {
   using G = Geo<D>;
   constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, kPiece);
   constexpr uint32_t idesc_o = tc_idesc_bf16(kTile, D) | (1u << 16);  // B with N contiguous
   const uint32_t base = smem_u32(smem) >> 4, tmem = uniform(c.tmem), vlo = (G::kHalfBytes >> 4) << 16, klo = 1u << 16;
-  const uint32_t empty = smem_u32(c.empty), s_full = smem_u32(c.s_full[w]);
+  const uint32_t empty = smem_u32(c.empty), s_full = smem_u32(c.s_full[w]), v_go = smem_u32(&c.v_go);
+  const uint32_t ts = tmem + s_cols(w, 0), to = tmem + o_cols(w);
   const uint32_t lead = elected();
   // The warp's lanes leave every wait together: one that fell behind could
-  // miss a phase of a barrier and wait for its parity for good.
+  // miss a phase of a barrier and wait for its parity for good.  Every tile of
+  // the ring is waited for, in order, for the same reason.
   auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL, wait(c, bar, parity, a.status)) != 0; };
   const int n_items = uniform(c.n_items);
   for (int k = 0; k < n_items; ++k) {
@@ -498,7 +500,6 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
     const bool both = uniform(both_in(it));
     const int lo = uniform(it.lo), tiles = uniform(it.hi) - lo;
     const int masked_from = uniform(it.masked_from) - lo * kTile, window_to = uniform(it.window_to) - lo * kTile;
-    const int steps = both ? 2 * tiles : tiles;
     // tile x of the item: K at ring position 2x, V at 2x + 1 from here on
     Ring kpos = st.k, vpos = st.k;
     vpos.advance<G::kStages>();
@@ -506,52 +507,91 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
     st.q_phase ^= 1;
     tc_fence_after();
     const uint32_t qd = (base + (G::kQ + (both ? w * G::kTileBytes : 0)) / 16) | klo;
-    for (int t = -2; t < steps; ++t) {
-      const int buf = t & 1, half = both ? buf : w;          // of step t and of step t + 2
-      const bool fresh = !both || buf == 0, last = !both || buf == 1;  // the group's first, its last use of a tile
-      if (t >= 0) {  // O += P V of step t
-        const int x = both ? t >> 1 : t;
-        const bool part = fresh && in_part(masked_from, window_to, x);
-        // Both warps wait for every tile of the ring, in order (a barrier's
-        // parity tells neighbouring phases apart, not those two laps apart),
-        // and send the tiles that need it to clean_v.
-        if (fresh && !ready(&c.full[vpos.stage], vpos.phase)) return false;
-        if (part) arrive_if(lead, smem_u32(&c.v_go));
-        if (!ready(&c.p_ready[w][buf], st.p_phase >> buf & 1)) return false;
-        st.p_phase ^= 1u << buf;
-        if (part) {
-          if (!ready(&c.v_ok, st.v_phase)) return false;
-          st.v_phase ^= 1;
-        }
-        tc_fence_after();
-        const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | vlo;
-        const uint32_t td = tmem + o_cols(w), ta = tmem + s_cols(w, buf);
+    auto qk = [&](int half, int buf) {  // S of a piece of K's tile
+      const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | klo;
 #pragma unroll
-        for (int e = 0; e < kPiece / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
-          mma_ts_if(lead, td, ta + e * 8, desc(vd + e * (2048 / 16)), idesc_o, t > 0 || e > 0);
-        if (last) {
-          commit_if(lead, empty + vpos.stage * 8);
-          vpos.advance<G::kStages>();
-          vpos.advance<G::kStages>();
+      for (int e = 0; e < D / 16; ++e) {
+        const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
+        mma_ss_if(lead, ts + buf * kPiece, desc(qd + off), desc(kd + off), idesc_s, e > 0);
+      }
+    };
+    auto pv = [&](int half, int buf, bool more) {  // O (+)= P V of a piece of V's tile
+      const uint32_t vd = (base + (G::kRing + vpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | vlo;
+#pragma unroll
+      for (int e = 0; e < kPiece / 16; ++e)  // 16 slots: 8 columns of P, two 1024-byte groups of V
+        mma_ts_if(lead, to, ts + buf * kPiece + e * 8, desc(vd + e * (2048 / 16)), idesc_o, more || e > 0);
+    };
+    auto p_ready = [&](int buf) {
+      if (!ready(&c.p_ready[w][buf], st.p_phase >> buf & 1)) return false;
+      st.p_phase ^= 1u << buf;
+      return true;
+    };
+    auto v_there = [&](int x) {  // tile x of V, and clean_v's go on it
+      if (!ready(&c.full[vpos.stage], vpos.phase)) return false;
+      if (in_part(masked_from, window_to, x)) {
+        arrive_if(lead, v_go);
+        if (!ready(&c.v_ok, st.v_phase)) return false;
+        st.v_phase ^= 1;
+      }
+      return true;
+    };
+    auto free_k = [&]() {
+      commit_if(lead, empty + kpos.stage * 8);
+      kpos.advance<G::kStages>();
+      kpos.advance<G::kStages>();
+    };
+    auto free_v = [&]() {
+      commit_if(lead, empty + vpos.stage * 8);
+      vpos.advance<G::kStages>();
+      vpos.advance<G::kStages>();
+    };
+    if (both) {
+      if (!ready(&c.full[kpos.stage], kpos.phase)) return false;
+      qk(0, 0);
+      commit_if(lead, s_full);
+      qk(1, 1);
+      commit_if(lead, s_full + 8);
+      free_k();
+      for (int x = 0; x < tiles; ++x) {
+        const bool next = x + 1 < tiles;
+        if (!v_there(x) || !p_ready(0)) return false;
+        tc_fence_after();
+        pv(0, 0, x > 0);
+        if (next) {
+          if (!ready(&c.full[kpos.stage], kpos.phase)) return false;
+          qk(0, 0);
+        }
+        commit_if(lead, s_full);
+        if (!p_ready(1)) return false;
+        tc_fence_after();
+        pv(1, 1, true);
+        if (next) qk(1, 1);
+        commit_if(lead, s_full + 8);
+        free_v();
+        if (next) free_k();
+      }
+    } else {
+      for (int x = 0; x < 2 && x < tiles; ++x) {
+        if (!ready(&c.full[kpos.stage], kpos.phase)) return false;
+        qk(w, x);
+        commit_if(lead, s_full + x * 8);
+        free_k();
+      }
+      for (int x = 0; x < tiles; ++x) {
+        const int buf = x & 1;
+        if (!v_there(x) || !p_ready(buf)) return false;
+        tc_fence_after();
+        pv(w, buf, x > 0);
+        free_v();
+        if (x + 2 < tiles) {
+          if (!ready(&c.full[kpos.stage], kpos.phase)) return false;
+          qk(w, buf);
+          commit_if(lead, s_full + buf * 8);
+          free_k();
+        } else {
+          commit_if(lead, s_full + buf * 8);
         }
       }
-      if (t + 2 < steps) {  // S = Q K^T of step t + 2
-        if (fresh && !ready(&c.full[kpos.stage], kpos.phase)) return false;
-        tc_fence_after();
-        const uint32_t kd = (base + (G::kRing + kpos.stage * G::kTileBytes + half * kPiece * 128) / 16) | klo;
-        const uint32_t ts = tmem + s_cols(w, buf);
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = (e / 4 * G::kHalfBytes + e % 4 * 32) / 16;
-          mma_ss_if(lead, ts, desc(qd + off), desc(kd + off), idesc_s, e > 0);
-        }
-        if (last) {
-          commit_if(lead, empty + kpos.stage * 8);
-          kpos.advance<G::kStages>();
-          kpos.advance<G::kStages>();
-        }
-      }
-      if (t >= 0 || t + 2 < steps) commit_if(lead, s_full + buf * 8);
     }
     // what this warp has seen (clean_v's word on the item), to the group
     arrive_if(lead, smem_u32(&c.o_full[w]));
@@ -684,9 +724,10 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
   const int tid = threadIdx.x - 128, w = tid / 128, r = tid % 128;
   const uint32_t lane_base = c.tmem + ((uint32_t)(r / 32 * 32) << 16);
   const uint32_t t_o = lane_base + o_cols(w);
-  QTile<D> q;
-  if (c.n_items > 0) load_q<D>(a, c.items[0], q);
-  for (int k = 0; k < c.n_items; ++k) {
+  const int n_items = c.n_items;
+  QTile<D> q = {};
+  if (n_items > 0) load_q<D>(a, c.items[0], q);
+  for (int k = 0; k < n_items; ++k) {
     const Item& it = c.items[k];
     const bool both = both_in(it);
     store_q<D>(smem, both, q);
@@ -777,7 +818,8 @@ __device__ __forceinline__ bool softmax_rows(const AttnArgs& a, uint8_t* smem, C
 
     // the output: every P V is done with the barriers of the two steps behind
     // the last one (the first of them is not there if there was only one step)
-    if (k + 1 < c.n_items) load_q<D>(a, c.items[k + 1], q);
+    q = QTile<D>{};  // what it held is not kept through the tiles
+    if (k + 1 < n_items) load_q<D>(a, c.items[k + 1], q);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int buf = (steps + x) & 1;
