@@ -49,7 +49,7 @@ extern "C" {
 /* The pools as mk_decode_step takes them: bf16 [n_layers][num_pages][n_kv]
  * [page_size][head_dim].  head_dim 64 or 128; page_size a power of two from
  * 16 to 256; the pools 16-byte aligned; num_pages * n_kv * page_size below
- * 2^31.  rope_base > 1: the rotation's base, as in mk_config. */
+ * 2^31.  A block table has at most 2^30 slots.  rope_base > 1: the rotation's base, as in mk_config. */
 typedef struct {
   int32_t n_layers, n_kv, page_size, head_dim;
   int64_t num_pages;

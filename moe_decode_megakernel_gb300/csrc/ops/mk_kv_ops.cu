@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
   if (!bad)
     for (int k = tid; k < m; k += kThreads) {
       const int s = path[k];
-      if (s < 0 || (k > 0 && s <= path[k - 1]) || (int64_t)ctx + s >= slots) {
+      if (s < k || (k > 0 && s <= path[k - 1]) || (int64_t)ctx + s >= slots) {  // s < k: it cannot ascend from 0
         bad = true;
         record(a.status, dev::ERR_INDEX, OP_COMMIT, b, k, s, (uint32_t)slots);
       } else {
@@ -398,7 +398,9 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
                  void* stream) {
   const int rc = check_tokens(kv, layer, tok);
   if (rc != MK_OK) return rc;
-  if (!io || !io->k || !io->v) return fail(MK_ERR_ARG, "null K or V");
+  if (!io) return fail(MK_ERR_ARG, "null argument");
+  if (tok->batch == 0 || tok->n_tokens == 0) return MK_OK;
+  if (!io->k || !io->v) return fail(MK_ERR_ARG, "null K or V");
   if (io->dtype != MK_BF16 && io->dtype != MK_F32) return fail(MK_ERR_ARG, "dtype is MK_BF16 or MK_F32");
   const mk_kv_config& c = kv->cfg;
   const size_t elem = io->dtype == MK_F32 ? 4 : 2;
@@ -429,7 +431,6 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
         collides(io->k, io->k_stride) || collides(io->v, io->v_stride))
       return fail(MK_ERR_ARG, "q_out overlaps an input");
   }
-  if (tok->batch == 0 || T == 0) return MK_OK;
   AppendArgs a;
   a.pools = pools_of(kv, layer);
   a.b = batch_of(tok);
@@ -449,7 +450,7 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
                  int32_t* new_lens, uint32_t* status, void* stream) {
   if (!kv) return fail(MK_ERR_ARG, "null argument");
   if (batch < 0 || max_path < 0 || max_pages < 1) return fail(MK_ERR_ARG, "negative batch or path width, or no page columns");
-  if (((int64_t)max_pages << kv->page_shift) > INT32_MAX) return fail(MK_ERR_ARG, "block tables of more than 2^31 - 1 slots");
+  if (!table_fits(kv, max_pages)) return fail(MK_ERR_ARG, "block tables of more than 2^30 slots");
   if (batch == 0) return MK_OK;
   if (!cache_lens || !path_lens || !block_tables || (max_path > 0 && !path)) return fail(MK_ERR_ARG, "null argument");
   if (batch > 65535) return fail(MK_ERR_ARG, "batch above 65535");
@@ -473,7 +474,7 @@ int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int3
   if (!kv) return fail(MK_ERR_ARG, "null argument");
   if (requests < 0 || beams < 1 || beams > kMaxBeams || max_pages < 1)
     return fail(MK_ERR_ARG, "bad number of requests, beams (1 to 64) or page columns");
-  if (((int64_t)max_pages << kv->page_shift) > INT32_MAX) return fail(MK_ERR_ARG, "block tables of more than 2^31 - 1 slots");
+  if (!table_fits(kv, max_pages)) return fail(MK_ERR_ARG, "block tables of more than 2^30 slots");
   if (requests == 0) return MK_OK;
   if (!lens || !parents || !tables_in || !tables_out) return fail(MK_ERR_ARG, "null argument");
   const size_t bytes = 4 * (size_t)requests * beams * max_pages;

@@ -164,12 +164,15 @@ inline Pools pools_of(const mk_kv* kv, int32_t layer) {
   return p;
 }
 
+// A sequence's slots (and a tile behind them) are counted in 32 bits.
+inline bool table_fits(const mk_kv* kv, int32_t max_pages) { return ((int64_t)max_pages << kv->page_shift) <= (int64_t)1 << 30; }
+
 // The checks that append and attention share.
 inline int check_tokens(const mk_kv* kv, int32_t layer, const mk_tokens* t) {
   if (!kv || !t) return fail(MK_ERR_ARG, "null argument");
   if (layer < 0 || layer >= kv->cfg.n_layers) return fail(MK_ERR_ARG, "layer outside the pools");
   if (t->batch < 0 || t->n_tokens < 0 || t->max_pages < 1) return fail(MK_ERR_ARG, "negative batch or token count, or no page columns");
-  if (((int64_t)t->max_pages << kv->page_shift) > INT32_MAX) return fail(MK_ERR_ARG, "block tables of more than 2^31 - 1 slots");
+  if (!table_fits(kv, t->max_pages)) return fail(MK_ERR_ARG, "block tables of more than 2^30 slots");
   if (t->batch > 0 && (!t->cu_seqlens || !t->cache_lens || !t->block_tables)) return fail(MK_ERR_ARG, "null batch array");
   return MK_OK;
 }

@@ -1170,7 +1170,9 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   int rc = check_tokens(kv, layer, tok);
   if (rc != MK_OK) return rc;
   const mk_kv_config& c = kv->cfg;
-  if (!io || !io->q || !io->out) return fail(MK_ERR_ARG, "null q or out");
+  if (!io) return fail(MK_ERR_ARG, "null argument");
+  if (tok->batch == 0 || tok->n_tokens == 0) return MK_OK;
+  if (!io->q || !io->out) return fail(MK_ERR_ARG, "null q or out");
   if (io->n_q < c.n_kv || io->n_q % c.n_kv != 0 || io->n_q > (1 << 16)) return fail(MK_ERR_ARG, "n_q must be a multiple of n_kv");
   if ((int64_t)tok->n_tokens * (io->n_q / c.n_kv) > INT32_MAX) return fail(MK_ERR_ARG, "more than 2^31 - 1 query rows per K/V head");
   const int64_t row = (int64_t)io->n_q * c.head_dim;
@@ -1182,9 +1184,14 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   if (io->tree_mask ? io->mask_words < 1 : io->mask_words != 0)
     return fail(MK_ERR_ARG, "mask_words must be positive with a tree_mask and 0 without");
   if (io->window < 0) return fail(MK_ERR_ARG, "negative window");
-  if (!(io->scale >= 0) || !std::isfinite(io->scale)) return fail(MK_ERR_ARG, "scale must be positive (0: 1 / sqrt(head_dim))");
+  if (!(io->scale >= 0) || !std::isfinite(io->scale * 1.5f)) return fail(MK_ERR_ARG, "scale must be positive (0: 1 / sqrt(head_dim))");
   if (!workspace || misaligned(workspace)) return fail(MK_ERR_ARG, "workspace null or misaligned");
-  if (tok->batch == 0 || tok->n_tokens == 0) return MK_OK;
+  const size_t lse_bytes = io->lse ? (size_t)tok->n_tokens * io->n_q * 4 : 0;
+  const size_t out_bytes = span(tok->n_tokens, io->out_stride, row, 2), q_bytes = span(tok->n_tokens, io->q_stride, row, 2);
+  if (overlap(workspace, workspace_bytes, io->out, out_bytes) || overlap(workspace, workspace_bytes, io->q, q_bytes) ||
+      overlap(workspace, workspace_bytes, io->lse, lse_bytes) || overlap(io->lse, lse_bytes, io->out, out_bytes) ||
+      overlap(io->lse, lse_bytes, io->q, q_bytes))
+    return fail(MK_ERR_ARG, "workspace or lse overlaps another argument");
   const int grid = grid_size();
   if (grid < 1) return fail(MK_ERR_CUDA, "no device");
   if (workspace_bytes < part_bytes(grid, c.head_dim)) return fail(MK_ERR_ARG, "workspace smaller than mk_tree_attn_workspace_bytes");

@@ -607,6 +607,19 @@ def test_commit_leaves_out_bad_paths():
     assert torch.equal(pg.k.cpu(), want)
 
 
+def test_commit_entries_in_front_of_their_place():
+    """A path that does not ascend may have entries whose place lies behind the table: nothing there is read."""
+    g = gen(33)
+    P = 16
+    pg = Paged(g, [16, 16], 1, P, 64, extra_cols=0)  # one column: slot 16 has none
+    k = pg.k.clone()
+    new_lens, st = torch.empty(2, dtype=torch.int32, device=DEV), new_status()
+    mk.kv_commit(pg.cache, ints([14, 14]), ints([[0, 0, 1], [0, 1, 1]]), ints([3, 3]), pg.tables, new_lens=new_lens, status=st)
+    with pytest.raises(mk.MkError):
+        mk.check_status(st)
+    assert new_lens.tolist() == [14, 14] and torch.equal(pg.k, k)
+
+
 # -------------------------------------------------------------------- select
 
 def run_select(logits, scores, n, finished=None, eos=-1):
@@ -932,3 +945,71 @@ def test_select_masked_vocabulary(low):
     check_select(got, logits, scores, n)
     for r in (0, 2):
         assert torch.equal(got[1][r].cpu().long(), beam[r]) and torch.equal(got[2][r].cpu().long(), token[r])
+
+
+def test_calls_with_nothing_to_do():
+    g = gen(81)
+    pg = Paged(g, [20], 2, 16, 64)
+    before = pg.k.clone()
+    ws = torch.empty(mk.tree_attn_workspace_bytes(pg.cache), dtype=torch.uint8, device=DEV)
+    e = lambda h: torch.empty(0, h, 64, dtype=BF, device=DEV)  # noqa: E731
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    for cu, cl, bt in ((ints([0, 0]), ints([5]), pg.tables), (ints([0]), none, pg.tables[:0])):
+        mk.kv_append(pg.cache, 0, e(2), e(2), cu, cl, bt, q=e(4), q_out=e(4))
+        mk.tree_attn(pg.cache, 0, e(4), e(4), cu, cl, bt, ws)
+    # tokens, but no sequence that has them
+    x = torch.ones(3, 2, 64, dtype=BF, device=DEV)
+    q = torch.ones(3, 4, 64, dtype=BF, device=DEV)
+    out = torch.full_like(q, 5.0)
+    mk.kv_append(pg.cache, 0, x, x, ints([0, 0]), ints([5]), pg.tables)
+    mk.tree_attn(pg.cache, 0, q, out, ints([3, 3]), ints([5]), pg.tables, ws)
+    mk.kv_commit(pg.cache, ints([5]), ints([[]]).view(1, 0), ints([0]), pg.tables, new_lens=(n := ints([0])))
+    assert n.tolist() == [5] and (out == 5).all() and torch.equal(pg.k, before)
+
+
+def test_first_call_of_a_handle_inside_a_capture():
+    g = gen(82)
+    pg = Paged(g, [300], 2, 64, 64)
+    q = torch.randn(3, 8, 64, generator=g, device=DEV).to(BF)
+    cu, cl = ints([0, 3]), ints([297])
+    want, _ = run_attn(pg, q, [297], [3])
+    cache = mk.KvCache(pg.k, pg.v, BASE)
+    out = torch.zeros_like(q)
+    ws = torch.empty(mk.tree_attn_workspace_bytes(cache), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        mk.tree_attn(cache, 0, q, out, cu, cl, pg.tables, ws)
+    assert (out == 0).all()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_many_sequences():
+    """More sequences than threads of a block or lanes of a warp, some without tokens, one cache."""
+    g = gen(83)
+    B, n_kv, d, P = 600, 2, 64, 16
+    new = [(7 * b) % 4 for b in range(B)]
+    ctx = [(13 * b) % 50 for b in range(B)]
+    pg = Paged(g, [a + n for a, n in zip(ctx, new)], n_kv, P, d)
+    T = sum(new)
+    qkv = torch.randn(T, 8, d, generator=g, device=DEV)
+    q_out = torch.empty(T, 4, d, dtype=BF, device=DEV)
+    st, cu, cl = new_status(), ints(starts(new)), ints(ctx)
+    mk.kv_append(pg.cache, 0, qkv[:, 4:6], qkv[:, 6:], cu, cl, pg.tables, q=qkv[:, :4], q_out=q_out, status=st)
+    out, lse = run_attn(pg, q_out, ctx, new, status=st)
+    mk.check_status(st)
+    check_attn(pg, q_out, out, lse, pg.tables, ctx, new, None, None, 0, 1 / math.sqrt(d), n_kv)
+    slot = torch.tensor([a + i for a, n in zip(ctx, new) for i in range(n)], device=DEV)
+    seq = torch.tensor([b for b, n in enumerate(new) for _ in range(n)], device=DEV)
+    assert torch.equal(pg.v[0][pg.tables.long()[seq, slot // P], :, slot % P], qkv[:, 6:].to(BF))
+    paths = [[n - 1] if n > 1 else [] for n in new]
+    new_lens = torch.empty(B, dtype=torch.int32, device=DEV)
+    want = pg.v.cpu()
+    for b, p in enumerate(paths):
+        plain.commit(want, pg.tables[b].tolist(), ctx[b], p)
+    mk.kv_commit(pg.cache, cl, ints([p + [0] * (1 - len(p)) for p in paths]), ints([len(p) for p in paths]), pg.tables,
+                 new_lens=new_lens, status=st)
+    mk.check_status(st)
+    assert torch.equal(pg.v.cpu(), want) and new_lens.tolist() == [a + len(p) for a, p in zip(ctx, paths)]

@@ -60,7 +60,7 @@ def tokens(**kw):
     return ops.MkTokens(**t)
 
 
-BAD_TOKENS = [dict(batch=-1), dict(n_tokens=-1), dict(max_pages=0), dict(max_pages=1 << 28), dict(cu_seqlens=None),
+BAD_TOKENS = [dict(batch=-1), dict(n_tokens=-1), dict(max_pages=0), dict(max_pages=(1 << 26) + 1), dict(cu_seqlens=None),
               dict(cache_lens=None), dict(block_tables=None)]
 
 
@@ -109,6 +109,8 @@ def test_null_handles():
 def test_nothing_to_do(kv):
     L = ops._lib()
     assert L.mk_kv_append(kv, 0, tokens(n_tokens=0), append_io(), None, None) == mk.MK_OK
+    assert L.mk_kv_append(kv, 0, tokens(n_tokens=0), append_io(k=None, v=None, q=None), None, None) == mk.MK_OK
+    assert L.mk_tree_attn(kv, 0, tokens(n_tokens=0), attn_io(q=None, out=None), None, 0, None, None) == mk.MK_OK
     assert L.mk_kv_append(kv, 0, tokens(batch=0, cu_seqlens=None), append_io(), None, None) == mk.MK_OK
     assert L.mk_tree_attn(kv, 0, tokens(n_tokens=0), attn_io(), 16 * A, 1 << 40, None, None) == mk.MK_OK
     assert L.mk_kv_commit(kv, 0, None, None, None, 0, None, 1, None, None, None) == mk.MK_OK
@@ -132,7 +134,8 @@ def test_attn_refuses_batches(kv, bad):
     dict(q=None), dict(out=None), dict(n_q=0), dict(n_q=1), dict(n_q=3), dict(n_q=-2), dict(q=4 * A + 8),
     dict(out=5 * A + 2), dict(q_stride=248), dict(q_stride=260), dict(out_stride=192), dict(out=4 * A), dict(out=4 * A + 512),
     dict(mask_words=0), dict(mask_words=-1), dict(tree_mask=None), dict(window=-1), dict(scale=-1.0),
-    dict(scale=float("nan")), dict(scale=float("inf"))])
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(lse=5 * A + 64), dict(lse=4 * A),
+    dict(lse=16 * A + 256), dict(out=16 * A + 256)])
 def test_attn_refuses(kv, bad):
     assert ops._lib().mk_tree_attn(kv, 0, tokens(), attn_io(**bad), 16 * A, 1 << 40, None, None) == mk.MK_ERR_ARG
     assert mk.last_error()
@@ -144,7 +147,7 @@ def test_attn_refuses_workspaces(kv, ws):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(batch=-1), dict(batch=65536), dict(max_path=-1), dict(max_pages=0), dict(cache_lens=None), dict(path=None),
+    dict(batch=-1), dict(batch=65536), dict(max_pages=(1 << 26) + 1), dict(max_path=-1), dict(max_pages=0), dict(cache_lens=None), dict(path=None),
     dict(path_lens=None), dict(block_tables=None), dict(new_lens=2 * A), dict(new_lens=2 * A + 4), dict(new_lens=4 * A)])
 def test_commit_refuses(kv, bad):
     a = dict(batch=2, cache_lens=2 * A, path=3 * A, path_lens=4 * A, max_path=4, block_tables=5 * A, max_pages=4, new_lens=6 * A)
@@ -154,7 +157,7 @@ def test_commit_refuses(kv, bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(requests=-1), dict(beams=0), dict(beams=65), dict(lens=None), dict(parents=None), dict(tables_in=None),
+    dict(requests=-1), dict(max_pages=(1 << 26) + 1), dict(beams=0), dict(beams=65), dict(lens=None), dict(parents=None), dict(tables_in=None),
     dict(tables_out=None), dict(max_pages=0), dict(tables_out=4 * A), dict(tables_out=4 * A + 100), dict(tables_out=3 * A)])
 def test_reorder_refuses(kv, bad):
     a = dict(requests=2, beams=4, lens=2 * A, parents=3 * A, tables_in=4 * A, tables_out=5 * A, max_pages=4)
