@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
   Parts<N>& sh = *reinterpret_cast<Parts<N>*>(raw);
   __shared__ float wm[kWarps];
   __shared__ double ws[kWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_before();
+  let_next_in();
   const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = a.n_out;
   const int lo = part * a.part_len, hi = min(a.vocab, lo + a.part_len);
   const float* x = a.logits + row * a.stride;
@@ -347,11 +348,12 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
     k.count = 0;
     k.tau = {0, 0};
   }
+  wait_before();
+  let_next_in();
   for (int w = tid; w < W; w += kThreads) {
     done[w] = a.finished && a.finished[r * W + w];
     scores[w] = a.scores[r * W + w];
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the first candidates on their way beside the parts' sums
   const uint64_t* keys = a.keys + (int64_t)r * N;
   const uint64_t early = tid < N ? keys[tid] : 0;
@@ -522,27 +524,14 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
   if (rc != MK_OK) return rc;
   const dim3 grid((unsigned)a.parts, (unsigned)rows);
   if (n_out <= 32) {
-    select_parts<32><<<grid, kThreads, sizeof(Parts<32>), st>>>(a);
+    rc = launch("select", select_parts<32>, grid, kThreads, sizeof(Parts<32>), st, a);
   } else {
     constexpr int wide = (int)sizeof(Parts<kMaxOut>);
     rc = allow_smem(wide_ready, reinterpret_cast<const void*>(&select_parts<kMaxOut>), wide, "select");
-    if (rc != MK_OK) return rc;
-    select_parts<kMaxOut><<<grid, kThreads, wide, st>>>(a);
+    if (rc == MK_OK) rc = launch("select", select_parts<kMaxOut>, grid, kThreads, wide, st, a);
   }
-  rc = launched("select");
   if (rc != MK_OK) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)requests);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute early;  // resident (waiting) before the last part is written
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, select_join, a);
-  return launched("select");
+  return launch("select", select_join, dim3((unsigned)requests), kThreads, smem, st, a);
 }
 
 }  // extern "C"

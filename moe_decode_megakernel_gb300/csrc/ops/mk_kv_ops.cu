@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   __shared__ int64_t row;  // row of head 0 in the pool, -1: not written
   __shared__ int pos, found;
   const int t = blockIdx.x, tid = threadIdx.x;
+  wait_before();
+  let_next_in();
   const int n_kv = a.pools.n_kv, heads = a.n_q + 2 * n_kv, chunks = heads * CPH;
   Chunk<F32> held[kHeld];
   auto load = [&](int base) {
@@ -163,6 +165,8 @@ constexpr int kHeld = 8;    // rows a thread holds between their loads and store
 __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitArgs a) {
   __shared__ int64_t from[kRound], to[kRound];  // rows of head 0, -1: nothing to do
   const int b = blockIdx.y, tid = threadIdx.x;
+  wait_before();
+  let_next_in();
   const int ctx = a.ctx[b], m = a.path_lens[b];
   const int32_t* path = a.path + (int64_t)b * a.max_path;
   const int32_t* table = a.tables + (int64_t)b * a.max_pages;
@@ -252,6 +256,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
   __shared__ int src[kMaxBeams], dst[kMaxBeams], mine[kMaxBeams];
   __shared__ int n_copy;
   const int r = blockIdx.x, tid = threadIdx.x, W = a.beams, P = 1 << a.pools.page_shift;
+  wait_before();
+  let_next_in();
   const int len = a.lens[r];
   const int32_t* tin = a.tables_in + (int64_t)r * W * a.max_pages;
   int32_t* tout = a.tables_out + (int64_t)r * W * a.max_pages;
@@ -441,8 +447,7 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
   for (int i = 0; i < 64; ++i) a.freq[i] = kv->freq[i];
   auto kernel = c.head_dim == 128 ? (io->dtype == MK_F32 ? append_kernel<128, true> : append_kernel<128, false>)
                                   : (io->dtype == MK_F32 ? append_kernel<64, true> : append_kernel<64, false>);
-  kernel<<<(unsigned)T, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched("append");
+  return launch("append", kernel, dim3((unsigned)T), kThreads, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, const int32_t* path,
@@ -465,8 +470,7 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
   const int64_t chunks = (int64_t)2 * kv->cfg.n_kv * a.row_chunks * kv->cfg.n_layers;
   if (chunks > INT32_MAX) return fail(MK_ERR_ARG, "more than 2^31 chunks in a token's rows");
   const dim3 grid((unsigned)((chunks + kThreads - 1) / kThreads), (unsigned)batch);
-  commit_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched("commit");
+  return launch("commit", commit_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int32_t* lens, const int32_t* parents,
@@ -489,8 +493,7 @@ int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int3
   const int64_t units = (int64_t)2 * kv->cfg.n_kv * kv->cfg.n_layers * beams;
   if (units > INT32_MAX) return fail(MK_ERR_ARG, "more than 2^31 runs to copy");
   const dim3 grid((unsigned)requests, 64);
-  reorder_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched("reorder");
+  return launch("reorder", reorder_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 int mk_check_status(const uint32_t* status, void* stream) {

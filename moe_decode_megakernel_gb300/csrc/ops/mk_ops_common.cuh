@@ -46,6 +46,11 @@ struct Batch {
   int32_t batch, n_tokens, max_pages;
 };
 
+// All earlier work of the stream is done and visible behind this.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may become resident once every block has passed this.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The first record stays: {code, operator, row, index, value, limit}.
 __device__ inline void record(uint32_t* status, uint32_t code, uint32_t op, uint32_t row, uint32_t index, uint32_t value,
                               uint32_t limit) {
@@ -130,9 +135,25 @@ inline size_t span(int64_t rows, int64_t stride, int64_t row_elems, size_t elem)
   return rows > 0 ? (size_t)((rows - 1) * stride + row_elems) * elem : 0;
 }
 
-inline int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+// Launches a kernel that may become resident while the one before it in the
+// stream ends; every such kernel waits (wait_before) before it touches memory.
+template <typename... P, typename... A>
+inline int launch(const char* what, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(MK_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+  }
   return MK_OK;
 }
 

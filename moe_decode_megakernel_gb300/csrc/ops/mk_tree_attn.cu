@@ -946,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl& c = *reinterpret_cast<Ctl*>(smem + G::kCtl);
   const int tid = threadIdx.x, warp = uniform(tid / 32);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_before();
+  let_next_in();
   if ((smem_u32(smem) & 1023) != 0) {  // the MMAs' layouts count on it
     if (tid == 0) {
       record(a.status, ERR_SMEM_ALIGN, OP_ATTN, 0, 0, smem_u32(smem), 1024);
@@ -1069,7 +1070,8 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
   constexpr int kWarps = kJoinThreads / 32, kHeld = 8;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, c = blockIdx.x + 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_before();
+  let_next_in();
   const Border& here = a.borders[c];
   const int64_t first = here.first, at = here.at;
   if (at >= first || a.borders[c - 1].first > at || (int)blockIdx.y * kJoinRows >= here.item.rows) return;
@@ -1122,28 +1124,17 @@ size_t part_bytes(int grid, int head_dim) {
 }
 
 template <int D>
-int launch(const AttnArgs& a, int grid, cudaStream_t st) {
+int launch_both(const AttnArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = Geo<D>::kCtl + (int)sizeof(Ctl);
   static_assert(smem <= 232448, "shared memory of a block");
   static std::atomic<uint64_t> ready{0};
   int rc = allow_smem(ready, reinterpret_cast<const void*>(&attn_kernel<D>), smem, "tree_attn");
   if (rc != MK_OK) return rc;
-  attn_kernel<D><<<grid, kThreads, smem, st>>>(a);
-  rc = launched("tree_attn");
+  rc = launch("tree_attn", attn_kernel<D>, dim3(grid), kThreads, smem, st, a);
   if (rc != MK_OK || grid == 1) return rc;
-  // the join may be resident (waiting) before the last parts are written
   const int64_t rows = (int64_t)a.b.n_tokens * a.group;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows, D / kJoinCols);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<D>, a, grid);
-  return launched("tree_attn");
+  const unsigned y = rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows;
+  return launch("tree_attn", join_kernel<D>, dim3(grid - 1, y, D / kJoinCols), kJoinThreads, 0, st, a, grid);
 }
 
 int grid_size() {
@@ -1212,7 +1203,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   a.status = status;
   a.tm_k = kv->tm_k, a.tm_v = kv->tm_v;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return c.head_dim == 128 ? launch<128>(a, grid, st) : launch<64>(a, grid, st);
+  return c.head_dim == 128 ? launch_both<128>(a, grid, st) : launch_both<64>(a, grid, st);
 }
 
 }  // extern "C"
