@@ -8,9 +8,9 @@
 // (sequence, head, query group, tile), are dealt to the SMs in runs of equal
 // cost: a unit for each tile, and three for the opening of each item (all tiles
 // of one query group): the fill and the drain of the pipeline and the output
-// cost about as much.  So a long
-// context is split over many SMs, a short one costs no more than it holds, and
-// nothing about the lengths is known to the host.  Where an item is cut by the
+// cost about as much.  So a long context is split over many SMs, a short one
+// costs no more than it holds, and nothing about the lengths is known to the
+// host.  Where an item is cut by the
 // border between two SMs, each leaves its part (row maxima, sums, unnormalised
 // outputs, fp32) in the workspace and a second kernel joins the parts in order.
 //
@@ -131,17 +131,6 @@ __device__ __forceinline__ int groups_of(const AttnArgs& a, const Seq& s) {
   return (s.n * a.group - 1) / kRows + (s.n > 0 ? 1 : 0);
 }
 
-// Tiles of one K/V head of a sequence.
-__device__ __forceinline__ int64_t tiles_in(const AttnArgs& a, const Seq& s) {
-  int64_t u = 0;
-  for (int m = 0, M = groups_of(a, s); m < M; ++m) {
-    int lo, hi;
-    tiles_of(a, s, m, lo, hi);
-    u += hi - lo;
-  }
-  return u;
-}
-
 __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t w = __shfl_up_sync(FULL, v, o);
@@ -159,11 +148,28 @@ struct Load {
   Seq s;
   int64_t tiles;
 };
+// (By all lanes of a warp: a prompt's many query groups are counted by all of
+// them, which took the plan of 2048 tokens from 15 to 4 us.)
 __device__ __forceinline__ Load load_of(const AttnArgs& a, int b) {
+  const int lane = threadIdx.x % 32;
   Load x = {{0, 0, 0}, 0};
-  if (b < a.b.batch) {
-    x.s = attn_seq(a, b);
-    x.tiles = tiles_in(a, x.s);
+  if (b < a.b.batch) x.s = attn_seq(a, b);
+  const int M = groups_of(a, x.s);
+  int lo, hi;
+  if (M == 1) {
+    tiles_of(a, x.s, 0, lo, hi);
+    x.tiles = hi - lo;
+  }
+  for (uint32_t many = __ballot_sync(FULL, M > 1); many; many &= many - 1) {
+    const int src = __ffs(many) - 1;
+    const Seq q = {__shfl_sync(FULL, x.s.t0, src), __shfl_sync(FULL, x.s.n, src), __shfl_sync(FULL, x.s.ctx, src)};
+    int64_t u = 0;
+    for (int m = lane, n = groups_of(a, q); m < n; m += 32) {
+      tiles_of(a, q, m, lo, hi);
+      u += hi - lo;
+    }
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
+    if (lane == src) x.tiles = u;
   }
   return x;
 }
@@ -178,8 +184,8 @@ __device__ __forceinline__ int64_t total_units(const AttnArgs& a, int grid, Load
   const int lane = threadIdx.x % 32;
   first = load_of(a, lane);
   int64_t u = first.tiles, items = groups_of(a, first.s);
-  for (int b = lane + 32; b < a.b.batch; b += 32) {
-    const Load x = load_of(a, b);
+  for (int b0 = 32; b0 < a.b.batch; b0 += 32) {
+    const Load x = load_of(a, b0 + lane);
     u += x.tiles;
     items += groups_of(a, x.s);
   }
@@ -197,8 +203,7 @@ __device__ __forceinline__ int64_t border(int64_t total, int c, int grid) {
   return base * c + (c < rest ? c : rest);
 }
 
-// The item of unit u at (h, m) of sequence b, whose units of this head begin
-// at unit `base`: everything but the part.
+// Item m of K/V head h of sequence b, whole.
 __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b, int h, int m) {
   Item it;
   it.b = b, it.h = h, it.t0 = s.t0, it.n = s.n, it.ctx = s.ctx;
@@ -208,16 +213,14 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
   const int i0 = (uint32_t)it.row0 / (uint32_t)a.group, i1 = (uint32_t)(it.row0 + it.rows - 1) / (uint32_t)a.group;
   it.masked_from = s.ctx + (a.mask ? 0 : i0 + 1);
   it.window_to = 0;
-  if (a.window) {
-    it.window_to = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
-  }
+  if (a.window) it.window_to = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
   it.slot = -1;
   return it;
 }
 
 // Calls f(item, unit of the item's first tile) for the items whose tiles lie in
-// units [u, end), in order, while it returns true.  By one warp, whose lanes hold the first
-// round's sequences; f runs on every lane.
+// units [u, end), in order, while it returns true.  By one warp, whose lanes
+// hold the first round's sequences; f runs on every lane.
 template <typename F>
 __device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, int opening, int64_t u, int64_t end, F f) {
   const int lane = threadIdx.x % 32;
@@ -238,7 +241,23 @@ __device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, 
       for (; h < a.pools.n_kv; ++h) {
         int64_t at = begin + h * ph;
         if (at >= end) return;
-        for (int m = 0; m < M; ++m) {
+        int m = 0;
+        if (at < u && M > 1) {  // the first group whose tiles end behind u
+          int64_t skipped = 0;
+          bool found = false;
+          for (m = 0; m < M && !found; m += 32) {
+            int lo = 0, hi = 0;
+            if (m + lane < M) tiles_of(a, q, m + lane, lo, hi);
+            const int64_t n = m + lane < M ? hi - lo + opening : 0, sum = warp_scan(n);
+            const uint32_t past = __ballot_sync(FULL, m + lane < M && at + skipped + sum > u);
+            found = past != 0;
+            const int j = found ? __ffs(past) - 1 : 31;
+            skipped += __shfl_sync(FULL, found ? sum - n : sum, j);
+            if (found) m += j - 32;
+          }
+          at += skipped;
+        }
+        for (; m < M; ++m) {
           int lo, hi;
           tiles_of(a, q, m, lo, hi);
           at += opening;
@@ -256,10 +275,9 @@ __device__ __forceinline__ void each_item(const AttnArgs& a, const Load& first, 
 
 // ------------------------------------------------------------- waits
 
-// (No function of the roles is called: a call fixes the registers of both
-// register budgets.)
 // Waits for a phase; false when this wait, or another one of the CTA, has
-// taken too long.
+// taken too long.  (Inlined like all the roles use: a function that is called
+// would have to keep to the smaller of their two register budgets.)
 __device__ __forceinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
   const int64_t until = gtimer() + kWaitNs;
   for (;;) {
@@ -1060,37 +1078,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
 constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinCols = kJoinThreads / 32 * 4, kMaxGrid = 160;
 
-// Block (c - 1, y, z): if the border between CTAs c - 1 and c of the first
-// kernel is the first one inside an item, joins 32 rows and 32 columns of that
-// item: the parts of CTAs c - 1, c, ... in order, four columns to a warp, a
-// row to a lane.  It is bound by the latency of its loads (a part's rows lie
-// side by side: 512 bytes per warp and load), so a thread has one output of
-// four columns and eight loads under way, and few parts share an SM.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  constexpr int kWarps = kJoinThreads / 32, kHeld = 8;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, c = blockIdx.x + 1;
+// A block joins 32 rows and 32 columns of an item that is cut (the border
+// between CTAs c - 1 and c of the first kernel is the first one inside it): the
+// parts of CTAs c - 1, c, ..., four columns to a warp, a row to a lane.  It is
+// bound by the latency of its loads (a part's rows lie side by side: 512 bytes
+// per warp and load).  kShare 1: block (c - 1, y, z), if that border is such a
+// one; a warp has eight parts under way.  kShare 4, for few items, whose parts
+// are many: block (k, y, z) takes the k-th cut, four warps share its parts and
+// meet in shared memory (38 parts of one sequence's four heads: 7.7 us with
+// kShare 1).
+template <int D, int kShare>
+__global__ void __launch_bounds__(kJoinThreads* kShare) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
+  constexpr int kWarps = kJoinThreads / 32, kHeld = kShare == 1 ? 8 : 4;
+  __shared__ float2 meet_ml[kShare == 1 ? 1 : kWarps * kShare][32];
+  __shared__ float4 meet_o[kShare == 1 ? 1 : kWarps * kShare][32];
+  __shared__ int cuts[kShare == 1 ? 1 : 32];
+  __shared__ int which;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   wait_before();
   let_next_in();
+  int c = blockIdx.x + 1;
+  if (kShare > 1) {
+    const bool cut = tid > 0 && tid < grid && a.borders[tid].at < a.borders[tid].first && a.borders[tid - 1].first <= a.borders[tid].at;
+    const uint32_t in = __ballot_sync(FULL, cut);
+    if (lane == 0) cuts[warp] = __popc(in);
+    if (tid == 0) which = 0;
+    __syncthreads();
+    int rank = __popc(in & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) rank += cuts[w];
+    if (cut && rank == (int)blockIdx.x) which = tid;
+    __syncthreads();
+    c = which;
+    if (c == 0) return;
+  }
   const Border& here = a.borders[c];
   const int64_t first = here.first, at = here.at;
   if (at >= first || a.borders[c - 1].first > at || (int)blockIdx.y * kJoinRows >= here.item.rows) return;
   const Item& item = here.item;
   const int64_t to = at + (item.hi - item.lo);
   const int parts = __syncthreads_count(tid < grid - (c - 1) && a.borders[c - 1 + tid].first < to);
-  const int row = blockIdx.y * kJoinRows + lane, col = blockIdx.z * kWarps + warp;  // columns in fours
+  const int row = blockIdx.y * kJoinRows + lane, col = blockIdx.z * kWarps + warp % kWarps;  // columns in fours
   float4 o = make_float4(0, 0, 0, 0);
   float top = -INFINITY, sum = 0.0f;
-  for (int k0 = 0; k0 < parts; k0 += kHeld) {
+  for (int k0 = warp / kWarps; k0 < parts; k0 += kHeld * kShare) {
     float2 ml[kHeld];
     float4 p[kHeld];
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
+      const int k = k0 + x * kShare;
       ml[x] = make_float2(-INFINITY, 0.0f);
       p[x] = make_float4(0, 0, 0, 0);
-      if (k0 + x < parts) {
+      if (k < parts) {
         // a part that begins its item is its CTA's last, the others their CTA's first
-        const int64_t s = 2 * (c - 1 + k0 + x) + (k0 + x == 0 ? 1 : 0);
+        const int64_t s = 2 * (c - 1 + k) + (k == 0 ? 1 : 0);
         ml[x] = a.part_ml[s * kRows + row];
         p[x] = a.part_o[(s * (D / 4) + col) * kRows + row];
       }
@@ -1104,10 +1144,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     top = up;
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
-      if (k0 + x >= parts) break;
+      if (k0 + x * kShare >= parts) break;
       const float f = ex2(ml[x].x - z);
       o.x += p[x].x * f, o.y += p[x].y * f, o.z += p[x].z * f, o.w += p[x].w * f;
       sum += ml[x].y * f;
+    }
+  }
+  if (kShare > 1) {
+    meet_ml[warp][lane] = make_float2(top, sum);
+    meet_o[warp][lane] = o;
+    __syncthreads();
+    if (warp >= kWarps) return;
+    float up = top;
+    for (int x = 1; x < kShare; ++x) up = fmaxf(up, meet_ml[warp + x * kWarps][lane].x);
+    const float z = up == -INFINITY ? 0.0f : up, by = ex2(top - z);
+    o.x *= by, o.y *= by, o.z *= by, o.w *= by;
+    sum *= by;
+    top = up;
+    for (int x = 1; x < kShare; ++x) {
+      const float2 ml = meet_ml[warp + x * kWarps][lane];
+      const float4 p = meet_o[warp + x * kWarps][lane];
+      const float f = ex2(ml.x - z);
+      o.x += p.x * f, o.y += p.y * f, o.z += p.z * f, o.w += p.w * f;
+      sum += ml.y * f;
     }
   }
   if (row >= item.rows) return;
@@ -1134,7 +1193,12 @@ int launch_both(const AttnArgs& a, int grid, cudaStream_t st) {
   if (rc != MK_OK || grid == 1) return rc;
   const int64_t rows = (int64_t)a.b.n_tokens * a.group;
   const unsigned y = rows < kRows ? (unsigned)((rows + kJoinRows - 1) / kJoinRows) : kRows / kJoinRows;
-  return launch("tree_attn", join_kernel<D>, dim3(grid - 1, y, D / kJoinCols), kJoinThreads, 0, st, a, grid);
+  // items at most: one for each K/V head of a sequence, and one more for every
+  // kRows query rows
+  const int64_t items = ((int64_t)a.b.batch + rows / kRows) * a.pools.n_kv;
+  if (items * 8 <= grid)  // eight parts or more to an item
+    return launch("tree_attn", join_kernel<D, 4>, dim3((unsigned)items, y, D / kJoinCols), kJoinThreads * 4, 0, st, a, grid);
+  return launch("tree_attn", join_kernel<D, 1>, dim3(grid - 1, y, D / kJoinCols), kJoinThreads, 0, st, a, grid);
 }
 
 int grid_size() {
