@@ -177,8 +177,8 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
  *  finished   device uint8 [requests][beams], nonzero: finished; or NULL
  *  out_*      device [requests][n_out]: scores fp32, parent beams int32,
  *             tokens int32; apart from the inputs
- * beams <= 64, n_out <= 128, n_out <= beams * vocab; with finished, 0 <= eos
- * < vocab. */
+ * beams <= 64, n_out <= 128, n_out <= beams * vocab <= 2^30; with finished,
+ * 0 <= eos < vocab. */
 size_t mk_beam_select_workspace_bytes(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out);
 int mk_beam_select(const float* logits, int64_t logits_stride, const float* scores,
                    const uint8_t* finished, int32_t eos, int32_t requests, int32_t beams,

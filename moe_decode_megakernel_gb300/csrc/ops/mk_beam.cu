@@ -468,9 +468,10 @@ int parts_of(int64_t rows, int vocab) {
   return (int)((tiles + per - 1) / per);
 }
 
+// The kernels count a row's logits in 32 bits, up to two tiles behind its end.
 bool shape_ok(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out) {
   return requests >= 0 && beams >= 1 && beams <= kMaxBeams && vocab >= 1 && n_out >= 1 && n_out <= kMaxOut &&
-         n_out <= (int64_t)beams * vocab && (int64_t)beams * vocab <= INT32_MAX && requests <= 1 << 20;
+         n_out <= (int64_t)beams * vocab && (int64_t)beams * vocab <= 1 << 30 && requests <= 1 << 20;
 }
 
 size_t sums_bytes(int64_t rows, int parts) { return (size_t)rows * parts * sizeof(double2); }
@@ -495,7 +496,7 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
                    int32_t eos, int32_t requests, int32_t beams, int32_t vocab, int32_t n_out, float* out_scores,
                    int32_t* out_parents, int32_t* out_tokens, void* workspace, size_t workspace_bytes, void* stream) {
   if (!shape_ok(requests, beams, vocab, n_out))
-    return fail(MK_ERR_ARG, "beams 1 to 64, n_out 1 to 128 and at most beams * vocab (below 2^31)");
+    return fail(MK_ERR_ARG, "beams 1 to 64, n_out 1 to 128 and at most beams * vocab (up to 2^30)");
   if (requests == 0) return MK_OK;
   if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return fail(MK_ERR_ARG, "null argument");
   if (logits_stride < vocab) return fail(MK_ERR_ARG, "logits_stride below vocab");

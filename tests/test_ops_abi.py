@@ -183,6 +183,14 @@ def test_select_refuses(bad):
     assert mk.last_error()
 
 
+@pytest.mark.parametrize("beams,vocab", [(1, (1 << 31) - 1), (1, (1 << 30) + 1), (4, (1 << 28) + 1), (64, 1 << 25)])
+def test_select_refuses_vocabularies_beyond_its_counters(beams, vocab):
+    a = dict(SELECT, beams=beams, vocab=vocab, stride=vocab, logits=1 << 44, bytes=1 << 40, requests=1, workspace=1 << 42)
+    assert ops._lib().mk_beam_select(*a.values(), None) == mk.MK_ERR_ARG
+    assert mk.beam_select_workspace_bytes(1, beams, vocab, 8) == 0
+    assert mk.beam_select_workspace_bytes(1, beams, (1 << 30) // beams, 8) > 0
+
+
 def test_select_workspace_sizes():
     f = mk.beam_select_workspace_bytes
     assert f(0, 65, 10, 1) == 0 and f(1, 1, 0, 1) == 0 and f(1, 1, 4, 5) == 0
