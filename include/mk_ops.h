@@ -18,9 +18,10 @@
  * allocated on the device, calls are asynchronous on `stream` and can be
  * captured into a graph, a bad argument returns MK_ERR_ARG before anything is
  * launched (mk_last_error()).  The tensors, the stream and the current device
- * have to be of one device.  Workspaces need no initialisation and hold
- * nothing between calls; calls (and replays of captured calls) that can
- * overlap in time need a workspace each.
+ * have to be of one device; an array's address is a multiple of its elements'
+ * size.  Workspaces lie apart from all other arguments, need no initialisation
+ * and hold nothing between calls; calls (and replays of captured calls) that
+ * can overlap in time need a workspace each.
  *
  * Values in device memory are checked on the device.  A call never reads or
  * writes outside the arrays it was given: what a value out of range would
@@ -157,7 +158,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
  * 1.  Each row of path ascends (0 <= path[b][0] < path[b][1] < ...).
  *  path       device int32 [batch][max_path]
  *  new_lens   device int32 [batch], receives cache_lens[b] + path_lens[b];
- *             not cache_lens itself; or NULL
+ *             apart from the inputs; or NULL
  * A sequence whose path does not ascend, is longer than max_path or leaves
  * its pages is left out (its new length is its cache length). */
 int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, const int32_t* path,

@@ -499,6 +499,7 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
     return fail(MK_ERR_ARG, "beams 1 to 64, n_out 1 to 128 and at most beams * vocab (up to 2^30)");
   if (requests == 0) return MK_OK;
   if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return fail(MK_ERR_ARG, "null argument");
+  if (misplaced(logits, scores, finished, out_scores, out_parents, out_tokens)) return fail(MK_ERR_ARG, "misaligned argument");
   if (logits_stride < vocab) return fail(MK_ERR_ARG, "logits_stride below vocab");
   if (finished && (eos < 0 || eos >= vocab)) return fail(MK_ERR_ARG, "eos outside the vocabulary");
   if (misaligned(workspace) || !workspace ||
@@ -512,6 +513,9 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
         overlap(outs[i], out, finished, (size_t)rows) || overlap(outs[i], out, outs[(i + 1) % 3], out) ||
         overlap(outs[i], out, workspace, workspace_bytes))
       return fail(MK_ERR_ARG, "an output overlaps another argument");
+  if (overlap(workspace, workspace_bytes, logits, in) || overlap(workspace, workspace_bytes, scores, row_bytes) ||
+      overlap(workspace, workspace_bytes, finished, (size_t)rows))
+    return fail(MK_ERR_ARG, "the workspace overlaps an input");
   SelectArgs a;
   a.logits = logits, a.stride = logits_stride, a.scores = scores, a.finished = finished, a.eos = eos;
   a.beams = beams, a.vocab = vocab, a.n_out = n_out;

@@ -417,6 +417,7 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
   if (!io) return fail(MK_ERR_ARG, "null argument");
   if (tok->batch == 0 || tok->n_tokens == 0) return MK_OK;
   if (!io->k || !io->v) return fail(MK_ERR_ARG, "null K or V");
+  if (misplaced(status)) return fail(MK_ERR_ARG, "misaligned status");
   if (io->dtype != MK_BF16 && io->dtype != MK_F32) return fail(MK_ERR_ARG, "dtype is MK_BF16 or MK_F32");
   const mk_kv_config& c = kv->cfg;
   const size_t elem = io->dtype == MK_F32 ? 4 : 2;
@@ -469,8 +470,11 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
   if (batch == 0) return MK_OK;
   if (!cache_lens || !path_lens || !block_tables || (max_path > 0 && !path)) return fail(MK_ERR_ARG, "null argument");
   if (batch > 65535) return fail(MK_ERR_ARG, "batch above 65535");
+  if (misplaced(cache_lens, path, path_lens, block_tables, new_lens, status)) return fail(MK_ERR_ARG, "misaligned argument");
   if (overlap(new_lens, 4 * (size_t)batch, cache_lens, 4 * (size_t)batch) ||
-      overlap(new_lens, 4 * (size_t)batch, path_lens, 4 * (size_t)batch))
+      overlap(new_lens, 4 * (size_t)batch, path_lens, 4 * (size_t)batch) ||
+      overlap(new_lens, 4 * (size_t)batch, path, 4 * (size_t)batch * max_path) ||
+      overlap(new_lens, 4 * (size_t)batch, block_tables, 4 * (size_t)batch * max_pages))
     return fail(MK_ERR_ARG, "new_lens overlaps an input");
   CommitArgs a;
   a.pools = pools_of(kv, 0);
@@ -491,6 +495,7 @@ int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int3
   if (!table_fits(kv, max_pages)) return fail(MK_ERR_ARG, "block tables of more than 2^30 slots");
   if (requests == 0) return MK_OK;
   if (!lens || !parents || !tables_in || !tables_out) return fail(MK_ERR_ARG, "null argument");
+  if (misplaced(lens, parents, tables_in, tables_out, status)) return fail(MK_ERR_ARG, "misaligned argument");
   const size_t bytes = 4 * (size_t)requests * beams * max_pages;
   if (overlap(tables_out, bytes, tables_in, bytes) || overlap(tables_out, bytes, parents, 4 * (size_t)requests * beams) ||
       overlap(tables_out, bytes, lens, 4 * (size_t)requests))
@@ -507,7 +512,7 @@ int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int3
 }
 
 int mk_check_status(const uint32_t* status, void* stream) {
-  if (!status) return fail(MK_ERR_ARG, "null argument");
+  if (!status || misplaced(status)) return fail(MK_ERR_ARG, "null or misaligned status");
   uint32_t r[8] = {};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(r, status, sizeof r, cudaMemcpyDeviceToHost, st);

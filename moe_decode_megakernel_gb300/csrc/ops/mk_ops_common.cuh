@@ -125,6 +125,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // ---------------------------------------------------------------- host side
 inline bool misaligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+// Whether an address (NULL aside) does not fit its elements.
+template <typename... T>
+inline bool misplaced(const T*... p) {
+  return (misaligned(p, sizeof(T)) || ...);
+}
+
 inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && an && bn && x < y + bn && y < x + an;
@@ -195,6 +201,7 @@ inline int check_tokens(const mk_kv* kv, int32_t layer, const mk_tokens* t) {
   if (t->batch < 0 || t->n_tokens < 0 || t->max_pages < 1) return fail(MK_ERR_ARG, "negative batch or token count, or no page columns");
   if (!table_fits(kv, t->max_pages)) return fail(MK_ERR_ARG, "block tables of more than 2^30 slots");
   if (t->batch > 0 && (!t->cu_seqlens || !t->cache_lens || !t->block_tables)) return fail(MK_ERR_ARG, "null batch array");
+  if (misplaced(t->cu_seqlens, t->cache_lens, t->block_tables, t->positions)) return fail(MK_ERR_ARG, "misaligned batch array");
   return MK_OK;
 }
 

@@ -1245,6 +1245,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
     return fail(MK_ERR_ARG, "misaligned q or out, or a stride that is too small or no multiple of 16 bytes");
   if (overlap(io->out, span(tok->n_tokens, io->out_stride, row, 2), io->q, span(tok->n_tokens, io->q_stride, row, 2)))
     return fail(MK_ERR_ARG, "out overlaps q");
+  if (misplaced(io->tree_mask, io->lse, status)) return fail(MK_ERR_ARG, "misaligned tree_mask, lse or status");
   if (io->tree_mask ? io->mask_words < 1 : io->mask_words != 0)
     return fail(MK_ERR_ARG, "mask_words must be positive with a tree_mask and 0 without");
   if (io->window < 0) return fail(MK_ERR_ARG, "negative window");

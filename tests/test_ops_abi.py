@@ -61,7 +61,8 @@ def tokens(**kw):
 
 
 BAD_TOKENS = [dict(batch=-1), dict(n_tokens=-1), dict(max_pages=0), dict(max_pages=(1 << 26) + 1), dict(cu_seqlens=None),
-              dict(cache_lens=None), dict(block_tables=None)]
+              dict(cache_lens=None), dict(block_tables=None), dict(cu_seqlens=A + 2), dict(cache_lens=2 * A + 1),
+              dict(block_tables=3 * A + 3), dict(positions=A + 1)]
 
 
 def append_io(**kw):
@@ -135,7 +136,7 @@ def test_attn_refuses_batches(kv, bad):
     dict(out=5 * A + 2), dict(q_stride=248), dict(q_stride=260), dict(out_stride=192), dict(out=4 * A), dict(out=4 * A + 512),
     dict(mask_words=0), dict(mask_words=-1), dict(tree_mask=None), dict(window=-1), dict(scale=-1.0),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(lse=5 * A + 64), dict(lse=4 * A),
-    dict(lse=16 * A + 256), dict(out=16 * A + 256)])
+    dict(lse=16 * A + 256), dict(out=16 * A + 256), dict(tree_mask=6 * A + 4), dict(lse=7 * A + 2)])
 def test_attn_refuses(kv, bad):
     assert ops._lib().mk_tree_attn(kv, 0, tokens(), attn_io(**bad), 16 * A, 1 << 40, None, None) == mk.MK_ERR_ARG
     assert mk.last_error()
@@ -148,7 +149,8 @@ def test_attn_refuses_workspaces(kv, ws):
 
 @pytest.mark.parametrize("bad", [
     dict(batch=-1), dict(batch=65536), dict(max_pages=(1 << 26) + 1), dict(max_path=-1), dict(max_pages=0), dict(cache_lens=None), dict(path=None),
-    dict(path_lens=None), dict(block_tables=None), dict(new_lens=2 * A), dict(new_lens=2 * A + 4), dict(new_lens=4 * A)])
+    dict(path_lens=None), dict(block_tables=None), dict(new_lens=2 * A), dict(new_lens=2 * A + 4), dict(new_lens=4 * A),
+    dict(new_lens=3 * A + 28), dict(new_lens=5 * A + 16), dict(new_lens=6 * A + 2), dict(path=3 * A + 1)])
 def test_commit_refuses(kv, bad):
     a = dict(batch=2, cache_lens=2 * A, path=3 * A, path_lens=4 * A, max_path=4, block_tables=5 * A, max_pages=4, new_lens=6 * A)
     a.update(bad)
@@ -158,7 +160,8 @@ def test_commit_refuses(kv, bad):
 
 @pytest.mark.parametrize("bad", [
     dict(requests=-1), dict(max_pages=(1 << 26) + 1), dict(beams=0), dict(beams=65), dict(lens=None), dict(parents=None), dict(tables_in=None),
-    dict(tables_out=None), dict(max_pages=0), dict(tables_out=4 * A), dict(tables_out=4 * A + 100), dict(tables_out=3 * A)])
+    dict(tables_out=None), dict(max_pages=0), dict(tables_out=4 * A), dict(tables_out=4 * A + 100), dict(tables_out=3 * A),
+    dict(tables_out=5 * A + 2), dict(lens=2 * A + 3)])
 def test_reorder_refuses(kv, bad):
     a = dict(requests=2, beams=4, lens=2 * A, parents=3 * A, tables_in=4 * A, tables_out=5 * A, max_pages=4)
     a.update(bad)
@@ -175,7 +178,9 @@ SELECT = dict(logits=A, stride=1000, scores=8 * A, finished=9 * A, eos=2, reques
     dict(beams=1, vocab=4, n_out=5), dict(vocab=1 << 30), dict(logits=None), dict(scores=None), dict(out_scores=None),
     dict(out_parents=None), dict(out_tokens=None), dict(stride=999), dict(eos=-1), dict(eos=1000), dict(workspace=None),
     dict(workspace=13 * A + 4), dict(bytes=100), dict(out_scores=8 * A), dict(out_scores=11 * A + 8),
-    dict(out_tokens=A + 64), dict(out_parents=9 * A), dict(out_scores=13 * A + 4), dict(requests=20000)])
+    dict(out_tokens=A + 64), dict(out_parents=9 * A), dict(out_scores=13 * A + 4), dict(requests=20000),
+    dict(logits=A + 2), dict(scores=8 * A + 1), dict(out_tokens=12 * A + 2), dict(workspace=8 * A - 4096, bytes=8192),
+    dict(workspace=9 * A - 4096, bytes=8192), dict(workspace=A + 1024, bytes=8192)])
 def test_select_refuses(bad):
     a = dict(SELECT)
     a.update(bad)
@@ -226,3 +231,12 @@ def test_binding_refuses_tensors():
         with pytest.raises(mk.MkError) as e:
             mk.tree_attn(c, 0, **{**good, **bad})
         assert e.value.code == mk.MK_ERR_ARG
+
+
+def test_status_addresses(kv):
+    L = ops._lib()
+    assert L.mk_kv_append(kv, 0, tokens(), append_io(), 15 * A + 2, None) == mk.MK_ERR_ARG
+    assert L.mk_tree_attn(kv, 0, tokens(), attn_io(), 16 * A, 1 << 40, 15 * A + 2, None) == mk.MK_ERR_ARG
+    assert L.mk_kv_commit(kv, 2, 2 * A, 3 * A, 4 * A, 4, 5 * A, 4, 6 * A, 15 * A + 2, None) == mk.MK_ERR_ARG
+    assert L.mk_beam_reorder(kv, 2, 4, 2 * A, 3 * A, 4 * A, 5 * A, 4, 15 * A + 2, None) == mk.MK_ERR_ARG
+    assert L.mk_check_status(15 * A + 2, None) == mk.MK_ERR_ARG
