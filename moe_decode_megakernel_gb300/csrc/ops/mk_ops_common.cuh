@@ -192,7 +192,8 @@ inline Pools pools_of(const mk_kv* kv, int32_t layer) {
 }
 
 // A sequence's slots (and a tile behind them) are counted in 32 bits.
-inline bool table_fits(const mk_kv* kv, int32_t max_pages) { return ((int64_t)max_pages << kv->page_shift) <= (int64_t)1 << 30; }
+constexpr int32_t kMaxSlots = 1 << 30;
+inline bool table_fits(const mk_kv* kv, int32_t max_pages) { return ((int64_t)max_pages << kv->page_shift) <= kMaxSlots; }
 
 // The checks that append and attention share.
 inline int check_tokens(const mk_kv* kv, int32_t layer, const mk_tokens* t) {

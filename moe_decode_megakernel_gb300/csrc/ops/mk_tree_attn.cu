@@ -1268,7 +1268,8 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   a.q = static_cast<const uint16_t*>(io->q), a.out = static_cast<uint16_t*>(io->out), a.lse = io->lse;
   a.mask = io->tree_mask;
   a.q_stride = io->q_stride, a.out_stride = io->out_stride;
-  a.n_q = io->n_q, a.group = io->n_q / c.n_kv, a.mask_words = io->mask_words, a.window = io->window;
+  a.n_q = io->n_q, a.group = io->n_q / c.n_kv, a.mask_words = io->mask_words;
+  a.window = io->window < kMaxSlots ? io->window : kMaxSlots;  // a longer one leaves nothing out, and differences stay in 32 bits
   a.layer = layer;
   a.scale_log2 = (float)((io->scale > 0 ? (double)io->scale : 1.0 / std::sqrt((double)c.head_dim)) * 1.4426950408889634);
   a.part_o = static_cast<float4*>(workspace);

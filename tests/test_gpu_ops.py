@@ -426,6 +426,25 @@ def test_attn_many_units(n_q, n_kv, d, P, ctx, new, kind, window):
         t += n
 
 
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1])
+@pytest.mark.parametrize("kind", [None, "tree"])
+def test_attn_windows_longer_than_any_cache(kind, window):
+    n_q, n_kv, d, ctx, new = 8, 2, 64, [300, 0], [150, 70]
+    g = gen(97)
+    pg = Paged(g, [a + b for a, b in zip(ctx, new)], n_kv, 64, d)
+    q = torch.randn(sum(new), n_q, d, generator=g, device=DEV).to(BF)
+    kw = {}
+    if kind:
+        trees = [tree_of(g, n, kind) for n in new]
+        kw = dict(tree_mask=mask_words([m for t in trees for m in t[0]], 3),
+                  positions=ints([c + e for c, t in zip(ctx, trees) for e in t[1]]))
+    st = new_status()
+    got = run_attn(pg, q, ctx, new, window=window, status=st, **kw)
+    want = run_attn(pg, q, ctx, new, **kw)
+    mk.check_status(st)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attn_extreme_scores():
     """Scores far apart (one slot takes all), equal ones, and the lowest: the running maximum must carry them."""
     g = gen(23)
