@@ -79,6 +79,18 @@ def _bad(msg: str):
     raise MkError(MK_ERR_ARG, msg)
 
 
+def _int32(v, name: str) -> int:
+    """v as the int32 that the call takes (ctypes would cut it off)."""
+    if not -1 << 31 <= v < 1 << 31:
+        _bad(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
+def _dims(t, name: str, n: int) -> None:
+    if t.dim() != n:
+        _bad(f"{name}: {n} dimensions are wanted, got {tuple(t.shape)}")
+
+
 def _take(t, name: str, dtype, shape, device):
     """The address of a contiguous tensor of this type, shape and device (None: NULL)."""
     if t is None:
@@ -146,8 +158,11 @@ class KvCache:
 
 def _tokens(cache, n_tokens, cu_seqlens, cache_lens, block_tables, positions):
     i32, dev = torch.int32, cache.device
-    batch, max_pages = cache_lens.shape[0], block_tables.shape[-1]
-    return MkTokens(batch, n_tokens, max_pages, _take(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
+    _dims(cache_lens, "cache_lens", 1)
+    _dims(block_tables, "block_tables", 2)
+    batch, max_pages = cache_lens.shape[0], block_tables.shape[1]
+    return MkTokens(_int32(batch, "batch"), _int32(n_tokens, "tokens"), _int32(max_pages, "page columns"),
+                    _take(cu_seqlens, "cu_seqlens", i32, (batch + 1,), dev),
                     _take(cache_lens, "cache_lens", i32, (batch,), dev),
                     _take(block_tables, "block_tables", i32, (batch, max_pages), dev),
                     _take(positions, "positions", i32, (n_tokens,), dev))
@@ -162,6 +177,7 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
     """mk_kv_append: k and v [tokens][n_kv][head_dim] (bf16 or fp32) into
     `layer` of the pools, k rotated; q [tokens][n_q][head_dim] of the same type
     rotated into q_out (bf16)."""
+    _dims(k, "k", 3)
     dev, T, d = cache.device, k.shape[0], cache.head_dim
     if k.dtype not in (torch.bfloat16, torch.float32):
         _bad(f"k: bf16 or fp32 is wanted, got {k.dtype}")
@@ -171,7 +187,8 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
         _bad("q and q_out go together")
     qp = qs = op = os_ = n_q = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[1] < 1:
+        _dims(q, "q", 3)
+        if q.shape[1] < 1:
             _bad(f"q: [tokens][heads][head_dim] is wanted, got {tuple(q.shape)}")
         n_q = q.shape[1]
         qp, qs = _rows(q, "q", k.dtype, (T, n_q, d), dev)
@@ -179,7 +196,7 @@ def kv_append(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, block_ta
     io = MkAppendIo(qp, kp, vp, op, qs, ks, vs, os_, n_q, MK_F32 if k.dtype is torch.float32 else MK_BF16)
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     st = _status(status, dev)
-    _call(_lib().mk_kv_append, dev, stream, cache.handle, layer, tok, io, st)
+    _call(_lib().mk_kv_append, dev, stream, cache.handle, _int32(layer, "layer"), tok, io, st)
 
 
 def tree_attn_workspace_bytes(cache: KvCache) -> int:
@@ -195,28 +212,37 @@ def tree_attn(cache: KvCache, layer: int, q, out, cu_seqlens, cache_lens, block_
     [tokens][words] (the bits of uint64 words) or None for a run of tokens;
     lse fp32 [tokens][n_q] or None; workspace uint8."""
     dev, bf = cache.device, torch.bfloat16
-    if q.dim() != 3:
-        _bad(f"q: [tokens][heads][head_dim] is wanted, got {tuple(q.shape)}")
+    _dims(q, "q", 3)
     T, n_q, _ = q.shape
-    if scale is not None and not scale > 0:
+    if scale is not None and not ctypes.c_float(scale).value > 0:  # as fp32: 0 would stand for the default
         _bad(f"scale must be positive, got {scale}")
     qp, qs = _rows(q, "q", bf, (T, n_q, cache.head_dim), dev)
     op, os_ = _rows(out, "out", bf, (T, n_q, cache.head_dim), dev)
-    words = 0 if tree_mask is None else tree_mask.shape[-1]
+    words = 0
+    if tree_mask is not None:  # without words it would have no address, as if there were none
+        _dims(tree_mask, "tree_mask", 2)
+        words = _int32(tree_mask.shape[1], "mask words")
+        if words < 1:
+            _bad("tree_mask: one word per token at least is wanted")
     io = MkAttnIo(qp, op, _take(lse, "lse", torch.float32, (T, n_q), dev),
-                  _take(tree_mask, "tree_mask", torch.int64, (T, words), dev), qs, os_, n_q, words, window,
+                  _take(tree_mask, "tree_mask", torch.int64, (T, words), dev), qs, os_, n_q, words,
+                  _int32(window, "window"),
                   0.0 if scale is None else scale)
     tok = _tokens(cache, T, cu_seqlens, cache_lens, block_tables, positions)
     ws = _take(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     st = _status(status, dev)
-    _call(_lib().mk_tree_attn, dev, stream, cache.handle, layer, tok, io, ws, workspace.numel(), st)
+    _call(_lib().mk_tree_attn, dev, stream, cache.handle, _int32(layer, "layer"), tok, io, ws, workspace.numel(), st)
 
 
 def kv_commit(cache: KvCache, cache_lens, path, path_lens, block_tables, new_lens=None, status=None,
               stream=None) -> None:
     """mk_kv_commit: path int32 [batch][max_path], path_lens int32 [batch]."""
     dev, i32 = cache.device, torch.int32
-    B, width, pages = cache_lens.shape[0], path.shape[-1], block_tables.shape[-1]
+    _dims(cache_lens, "cache_lens", 1)
+    _dims(path, "path", 2)
+    _dims(block_tables, "block_tables", 2)
+    B, width = _int32(cache_lens.shape[0], "batch"), _int32(path.shape[1], "path width")
+    pages = _int32(block_tables.shape[1], "page columns")
     args = (_take(cache_lens, "cache_lens", i32, (B,), dev), _take(path, "path", i32, (B, width), dev),
             _take(path_lens, "path_lens", i32, (B,), dev), width,
             _take(block_tables, "block_tables", i32, (B, pages), dev), pages,
@@ -238,12 +264,12 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, 
     dev, f32, i32 = logits.device, torch.float32, torch.int32
     if scores.dim() != 2 or logits.dim() != 2 or out_scores.dim() != 2:
         _bad("logits, scores and outputs have two dimensions")
-    (R, W), V, n = scores.shape, logits.shape[1], out_scores.shape[1]
+    (R, W), V, n = scores.shape, _int32(logits.shape[1], "vocab"), out_scores.shape[1]
     if logits.dtype is not f32 or logits.shape[0] != R * W or (V > 1 and logits.stride(1) != 1):
         _bad(f"logits: fp32 [{R * W}][vocab] with the vocabulary side by side is wanted, got {logits.dtype} "
              f"{tuple(logits.shape)} strides {logits.stride()}")
     args = (logits.stride(0) if R * W > 1 else V, _take(scores, "scores", f32, (R, W), dev),
-            _take(finished, "finished", torch.uint8, (R, W), dev), eos, R, W, V, n,
+            _take(finished, "finished", torch.uint8, (R, W), dev), _int32(eos, "eos"), R, W, V, n,
             _take(out_scores, "out_scores", f32, (R, n), dev), _take(out_parents, "out_parents", i32, (R, n), dev),
             _take(out_tokens, "out_tokens", i32, (R, n), dev),
             _take(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel())
@@ -254,9 +280,9 @@ def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=No
     """mk_beam_reorder: lens int32 [requests], parents int32
     [requests][beams], tables int32 [requests * beams][max_pages]."""
     dev, i32 = cache.device, torch.int32
-    if parents.dim() != 2:
-        _bad(f"parents: [requests][beams] is wanted, got {tuple(parents.shape)}")
-    (R, W), pages = parents.shape, tables_in.shape[-1]
+    _dims(parents, "parents", 2)
+    _dims(tables_in, "tables_in", 2)
+    (R, W), pages = parents.shape, _int32(tables_in.shape[1], "page columns")
     args = (R, W, _take(lens, "lens", i32, (R,), dev), _take(parents, "parents", i32, (R, W), dev),
             _take(tables_in, "tables_in", i32, (R * W, pages), dev),
             _take(tables_out, "tables_out", i32, (R * W, pages), dev), pages, _status(status, dev))

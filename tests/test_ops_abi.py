@@ -240,3 +240,46 @@ def test_status_addresses(kv):
     assert L.mk_kv_commit(kv, 2, 2 * A, 3 * A, 4 * A, 4, 5 * A, 4, 6 * A, 15 * A + 2, None) == mk.MK_ERR_ARG
     assert L.mk_beam_reorder(kv, 2, 4, 2 * A, 3 * A, 4 * A, 5 * A, 4, 15 * A + 2, None) == mk.MK_ERR_ARG
     assert L.mk_check_status(15 * A + 2, None) == mk.MK_ERR_ARG
+
+
+def test_binding_refuses_what_ctypes_would_take():
+    """Integers of more than 32 bits, a scale that is 0 as fp32, a mask without words (no address: a run),
+    tensors of other dimensions; by a stand-in for the device, so that only the binding refuses."""
+    import torch
+
+    class Fake:
+        device, n_layers, n_kv, head_dim, handle = torch.device("cpu"), 2, 2, 64, None
+    bf, c, w = torch.bfloat16, Fake(), torch.zeros(64, dtype=torch.uint8)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    q, k = torch.zeros(4, 4, 64, dtype=bf), torch.zeros(4, 2, 64, dtype=bf)
+    batch = dict(cu_seqlens=i(3), cache_lens=i(2), block_tables=i(2, 4))
+    ops._lib()
+
+    def refused(f, *args, **kw):
+        with pytest.raises(mk.MkError) as e:
+            f(*args, **kw)
+        assert e.value.code == mk.MK_ERR_ARG
+        return "a CUDA device is wanted" not in str(e.value)  # the check that every call here ends with
+    attn = dict(q=q, out=torch.empty_like(q), workspace=w, **batch)
+    assert not refused(mk.tree_attn, c, 0, **attn)
+    for bad in (dict(window=(1 << 32) + 5), dict(window=1 << 31), dict(scale=1e-50), dict(scale=float("nan")),
+                dict(tree_mask=torch.zeros(4, 0, dtype=torch.int64)), dict(tree_mask=torch.tensor(0)),
+                dict(cache_lens=torch.tensor(0, dtype=torch.int32)), dict(block_tables=i(8))):
+        assert refused(mk.tree_attn, c, 0, **{**attn, **bad}), bad
+    assert refused(mk.tree_attn, c, 1 << 32, **attn)
+    append = dict(k=k, v=k.clone(), **batch)
+    assert not refused(mk.kv_append, c, 0, **append)
+    assert refused(mk.kv_append, c, 1 << 32, **append) and refused(mk.kv_append, c, 0, **{**append, "k": torch.tensor(1.0)})
+    wide = torch.zeros(1, dtype=torch.int32).expand(1 << 33).unflatten(0, (2, 1 << 32))  # no memory behind it
+    assert refused(mk.kv_append, c, 0, **{**append, "block_tables": wide})
+    commit = (i(2), i(2, 3), i(2), i(2, 4))
+    assert not refused(mk.kv_commit, c, *commit)
+    for at, bad in ((0, torch.tensor(0)), (1, i(6)), (3, i(8)), (1, wide), (3, wide)):
+        assert refused(mk.kv_commit, c, *commit[:at], bad, *commit[at + 1:])
+    assert not refused(mk.beam_reorder, c, i(2), i(2, 4), i(8, 3), i(8, 3))
+    assert refused(mk.beam_reorder, c, i(2), i(2, 4), torch.tensor(0), i(8, 3))
+    select = dict(logits=torch.zeros(2, 8), scores=torch.zeros(1, 2), out_scores=torch.zeros(1, 4), out_parents=i(1, 4),
+                  out_tokens=i(1, 4), workspace=w)
+    assert not refused(mk.beam_select, **select)
+    assert refused(mk.beam_select, **select, eos=1 << 32)
+    assert refused(mk.beam_select, **{**select, "logits": torch.zeros(1).expand(1 << 33).unflatten(0, (2, 1 << 32))})
