@@ -71,15 +71,16 @@ __device__ __forceinline__ void values(const Chunk<false>& c, float (&x)[8]) {
 // chunks of every thread are on their way before the token's slot is known
 // (its sequence, then its page: two round trips to memory); the thread whose
 // sequence holds the token looks the slot up, half a head of threads turns the
-// position into sines.  12.6K tokens of 40 heads of 128 (258 MB moved) take 47
-// us, 5.4 TB/s where a copy of that size reaches 6.8: bound by memory.  (Runs
-// of tokens per block, the next token's chunks under way, took the same 47.5;
-// a single chunk at a time 49.4.)  Eight tokens are a chain of four round
-// trips, about 5 us.
+// position into sines.  12.6K tokens of 40 heads of 128 (258 MB moved) take 42
+// us, 6.2 TB/s where a copy of that size reaches 6.8: bound by memory.  Small
+// blocks with many chunks of a thread under way: 256 threads with three took 48
+// us, 128 with three 44; 64 with ten were no faster.
+// Eight tokens are a chain of four round trips, about 5 us.
+constexpr int kAppend = 128;
 template <int D, bool F32>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppend) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int CPH = D / 8;  // chunks per head
-  constexpr int kHeld = 3;    // chunks of a thread under way
+  constexpr int kHeld = 5;    // chunks of a thread under way
   __shared__ float2 cs[D / 2];
   __shared__ int64_t row;  // row of head 0 in the pool, -1: not written
   __shared__ int pos, found;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   auto load = [&](int base) {
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
-      const int i = base + x * kThreads + tid, h = i / CPH, c = i % CPH;
+      const int i = base + x * kAppend + tid, h = i / CPH, c = i % CPH;
       if (i >= chunks) break;
       if (h < a.n_q)
         held[x] = load8<F32>(a.q, t * a.q_stride + h * D + c * 8);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   load(0);
   if (tid == 0) found = 0;
   __syncthreads();
-  for (int b = tid; b < a.b.batch; b += kThreads) {
+  for (int b = tid; b < a.b.batch; b += kAppend) {
     if (a.b.cu[b] > t || t >= a.b.cu[b + 1]) continue;
     const Seq s = seq_of(a.b, b, a.pools.page_shift, a.status, OP_APPEND);
     if (s.n == 0) continue;
@@ -122,11 +123,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   if (!found) return;
   if (tid < D / 2) cs[tid] = turn(a.freq[tid], pos);
   __syncthreads();
-  for (int base = 0; base < chunks; base += kHeld * kThreads) {
+  for (int base = 0; base < chunks; base += kHeld * kAppend) {
     if (base) load(base);
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
-      const int i = base + x * kThreads + tid, h = i / CPH, c = i % CPH;
+      const int i = base + x * kAppend + tid, h = i / CPH, c = i % CPH;
       if (i >= chunks || (h >= a.n_q && row < 0)) break;
       float v[8];
       values(held[x], v);
@@ -458,7 +459,7 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
   for (int i = 0; i < 64; ++i) a.freq[i] = kv->freq[i];
   auto kernel = c.head_dim == 128 ? (io->dtype == MK_F32 ? append_kernel<128, true> : append_kernel<128, false>)
                                   : (io->dtype == MK_F32 ? append_kernel<64, true> : append_kernel<64, false>);
-  return launch("append", kernel, dim3((unsigned)T), kThreads, 0, static_cast<cudaStream_t>(stream), a);
+  return launch("append", kernel, dim3((unsigned)T), kAppend, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, const int32_t* path,
