@@ -32,9 +32,9 @@
 // make its next one and the other group's.
 //
 // Measured on a GB300 (heads of 128, 8 query heads to a K/V head, BF16): 32
-// trees of up to 16 tokens over 512 to 32K slots 186 us, 1.09 GB of K and V at
-// 5.8 TB/s (a copy: 6.8), bound by memory; 2048 tokens of a run over 8K slots
-// 240 us, 1.29 PFLOP/s (cuBLAS: 1.9), the tensor pipe active 64% of the
+// trees of up to 16 tokens over 512 to 32K slots 181 us, 1.09 GB of K and V at
+// 6.0 TB/s (a copy: 6.8), bound by memory; 2048 tokens of a run over 8K slots
+// 232 us, 1.33 PFLOP/s (cuBLAS: 1.9), the tensor pipe active 64% of the
 // kernel's cycles, bound by the hand-overs between exponentials and MMAs (a
 // step of 64 slots takes a group some 1730 cycles, of which its own and the
 // other group's MMAs run 1024); eight tokens over 8K slots 19 us: 2.6 the
@@ -1087,18 +1087,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
 constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinCols = kJoinThreads / 32 * 4, kMaxGrid = 160;
 
-// A block joins 32 rows and 32 columns of an item that is cut (the border
-// between CTAs c - 1 and c of the first kernel is the first one inside it): the
-// parts of CTAs c - 1, c, ..., four columns to a warp, a row to a lane.  It is
-// bound by the latency of its loads (a part's rows lie side by side: 512 bytes
-// per warp and load).  kShare 1: block (c - 1, y, z), if that border is such a
-// one; a warp has eight parts under way.  kShare 4, for few items, whose parts
-// are many: block (k, y, z) takes the k-th cut, four warps share its parts and
-// meet in shared memory (38 parts of one sequence's four heads: 7.7 us with
-// kShare 1).
+// A block joins 32 rows of an item that is cut (the border between CTAs c - 1
+// and c of the first kernel is the first one inside it): the parts of CTAs c -
+// 1, c, ..., four columns to a warp, a row to a lane.  It is bound by the
+// latency of its loads (a part's rows lie side by side: 512 bytes per warp and
+// load).  kShare 1: block (c - 1, y), if that border is such a one, for all
+// columns, two parts under way: most items have no more, and few blocks are
+// few rounds of latency (a 2048-token run 232 us as a whole; 241 with eight
+// parts under way in blocks of 32 columns, 234 with two; items of 38 parts
+// among others take 2 us longer).  kShare 4, for few items, whose parts are
+// many: block (k, y, z) takes the k-th cut and 32 columns, four warps share its
+// parts and meet in shared memory (38 parts of one sequence's four heads: 7.7
+// us with eight parts under way and kShare 1).
 template <int D, int kShare>
 __global__ void __launch_bounds__(kJoinThreads* kShare) join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  constexpr int kWarps = kJoinThreads / 32, kHeld = kShare == 1 ? 8 : 4;
+  constexpr int kWarps = kJoinThreads / 32, kHeld = kShare == 1 ? 2 : 4;  // parts under way
+  constexpr int kQuads = kShare == 1 ? D / kJoinCols : 1;  // fours of columns of a thread
   __shared__ float2 meet_ml[kShare == 1 ? 1 : kWarps * kShare][32];
   __shared__ float4 meet_o[kShare == 1 ? 1 : kWarps * kShare][32];
   __shared__ int cuts[kShare == 1 ? 1 : 32];
@@ -1126,55 +1130,60 @@ __global__ void __launch_bounds__(kJoinThreads* kShare) join_kernel(const __grid
   const Item& item = here.item;
   const int64_t to = at + (item.hi - item.lo);
   const int parts = __syncthreads_count(tid < grid - (c - 1) && a.borders[c - 1 + tid].first < to);
-  const int row = blockIdx.y * kJoinRows + lane, col = blockIdx.z * kWarps + warp % kWarps;  // columns in fours
-  float4 o = make_float4(0, 0, 0, 0);
+  const int row = blockIdx.y * kJoinRows + lane, col = blockIdx.z * kWarps * kQuads + warp % kWarps;  // columns in fours
+  float4 o[kQuads];
+#pragma unroll
+  for (int y = 0; y < kQuads; ++y) o[y] = make_float4(0, 0, 0, 0);
   float top = -INFINITY, sum = 0.0f;
   for (int k0 = warp / kWarps; k0 < parts; k0 += kHeld * kShare) {
     float2 ml[kHeld];
-    float4 p[kHeld];
+    float4 p[kHeld][kQuads];
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
       const int k = k0 + x * kShare;
       ml[x] = make_float2(-INFINITY, 0.0f);
-      p[x] = make_float4(0, 0, 0, 0);
       if (k < parts) {
         // a part that begins its item is its CTA's last, the others their CTA's first
         const int64_t s = 2 * (c - 1 + k) + (k == 0 ? 1 : 0);
         ml[x] = a.part_ml[s * kRows + row];
-        p[x] = a.part_o[(s * (D / 4) + col) * kRows + row];
+#pragma unroll
+        for (int y = 0; y < kQuads; ++y) p[x][y] = a.part_o[(s * (D / 4) + col + y * kWarps) * kRows + row];
       }
     }
     float up = top;
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) up = fmaxf(up, ml[x].x);
     const float z = up == -INFINITY ? 0.0f : up, by = ex2(top - z);
-    o.x *= by, o.y *= by, o.z *= by, o.w *= by;
+#pragma unroll
+    for (int y = 0; y < kQuads; ++y) o[y].x *= by, o[y].y *= by, o[y].z *= by, o[y].w *= by;
     sum *= by;
     top = up;
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
       if (k0 + x * kShare >= parts) break;
       const float f = ex2(ml[x].x - z);
-      o.x += p[x].x * f, o.y += p[x].y * f, o.z += p[x].z * f, o.w += p[x].w * f;
+#pragma unroll
+      for (int y = 0; y < kQuads; ++y)
+        o[y].x += p[x][y].x * f, o[y].y += p[x][y].y * f, o[y].z += p[x][y].z * f, o[y].w += p[x][y].w * f;
       sum += ml[x].y * f;
     }
   }
   if (kShare > 1) {
     meet_ml[warp][lane] = make_float2(top, sum);
-    meet_o[warp][lane] = o;
+    meet_o[warp][lane] = o[0];
     __syncthreads();
     if (warp >= kWarps) return;
     float up = top;
     for (int x = 1; x < kShare; ++x) up = fmaxf(up, meet_ml[warp + x * kWarps][lane].x);
     const float z = up == -INFINITY ? 0.0f : up, by = ex2(top - z);
-    o.x *= by, o.y *= by, o.z *= by, o.w *= by;
+    o[0].x *= by, o[0].y *= by, o[0].z *= by, o[0].w *= by;
     sum *= by;
     top = up;
     for (int x = 1; x < kShare; ++x) {
       const float2 ml = meet_ml[warp + x * kWarps][lane];
       const float4 p = meet_o[warp + x * kWarps][lane];
       const float f = ex2(ml.x - z);
-      o.x += p.x * f, o.y += p.y * f, o.z += p.z * f, o.w += p.w * f;
+      o[0].x += p.x * f, o[0].y += p.y * f, o[0].z += p.z * f, o[0].w += p.w * f;
       sum += ml.y * f;
     }
   }
@@ -1183,7 +1192,9 @@ __global__ void __launch_bounds__(kJoinThreads* kShare) join_kernel(const __grid
   const int i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint16_t* dst = a.out + (int64_t)(item.t0 + i) * a.out_stride + (int64_t)(item.h * a.group + g) * D;
-  *reinterpret_cast<uint2*>(dst + col * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+#pragma unroll
+  for (int y = 0; y < kQuads; ++y)
+    *reinterpret_cast<uint2*>(dst + (col + y * kWarps) * 4) = make_uint2(pack_bf16(o[y].x * inv, o[y].y * inv), pack_bf16(o[y].z * inv, o[y].w * inv));
   if (col == 0 && a.lse) a.lse[(int64_t)(item.t0 + i) * a.n_q + item.h * a.group + g] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
@@ -1207,7 +1218,7 @@ int launch_both(const AttnArgs& a, int grid, cudaStream_t st) {
   const int64_t items = ((int64_t)a.b.batch + rows / kRows) * a.pools.n_kv;
   if (items * 8 <= grid)  // eight parts or more to an item
     return launch("tree_attn", join_kernel<D, 4>, dim3((unsigned)items, y, D / kJoinCols), kJoinThreads * 4, 0, st, a, grid);
-  return launch("tree_attn", join_kernel<D, 1>, dim3(grid - 1, y, D / kJoinCols), kJoinThreads, 0, st, a, grid);
+  return launch("tree_attn", join_kernel<D, 1>, dim3(grid - 1, y), kJoinThreads, 0, st, a, grid);
 }
 
 int grid_size() {
