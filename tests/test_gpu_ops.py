@@ -796,6 +796,25 @@ def test_reorder(n_kv, d, P, layers, W):
     assert torch.equal(pg.k.cpu(), want[0]) and torch.equal(pg.v.cpu(), want[1])
 
 
+@pytest.mark.parametrize("R,W,layers,n_kv", [(700, 2, 2, 1), (300, 3, 3, 4), (1, 4, 30, 8), (90, 5, 4, 2), (20, 4, 20, 8)])
+def test_reorder_few_and_many_requests(R, W, layers, n_kv):
+    """Copies dealt to 8 up to hundreds of blocks per request, several units or less than one to a block."""
+    import random
+    r, P = random.Random(R), 16
+    lens = [r.randrange(3 * P) for _ in range(R)]
+    lens[0] = P + 5
+    pg = Paged(gen(53), [3 * P] * (R * W), n_kv, P, 64, layers=layers)
+    parents = [[r.randrange(W) for _ in range(W)] for _ in range(R)]
+    tables = pg.tables.view(R, W, -1).cpu()
+    want = [pg.k.cpu(), pg.v.cpu()]
+    new = plain.reorder(want, tables, lens, parents, P)
+    out, st = torch.full_like(pg.tables, -7), new_status()
+    mk.beam_reorder(pg.cache, ints(lens), ints(parents), pg.tables, out, status=st)
+    mk.check_status(st)
+    assert torch.equal(out.cpu().view(R, W, -1), new)
+    assert torch.equal(pg.k.cpu(), want[0]) and torch.equal(pg.v.cpu(), want[1])
+
+
 def test_reorder_leaves_out_what_is_out_of_range():
     g = gen(52)
     P, W = 16, 3
