@@ -220,7 +220,10 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& s, int b
   it.rows = s.n * a.group - it.row0 < kRows ? s.n * a.group - it.row0 : kRows;
   tiles_of(a, s, m, it.lo, it.hi);
   const int i0 = (uint32_t)it.row0 / (uint32_t)a.group, i1 = (uint32_t)(it.row0 + it.rows - 1) / (uint32_t)a.group;
-  it.masked_from = s.ctx + (a.mask ? 0 : i0 + 1);
+  // without a mask every row sees the new tokens up to the first row's own,
+  // unless positions set them a window or more apart
+  const bool apart = a.window && a.b.positions && s.n > a.window;
+  it.masked_from = s.ctx + (a.mask || apart ? 0 : i0 + 1);
   it.window_to = 0;
   if (a.window) it.window_to = s.ctx + (a.b.positions ? s.n - 1 : i1) - a.window + 1;  // the highest row's lowest slot
   it.slot = -1;

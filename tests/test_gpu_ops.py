@@ -1051,3 +1051,49 @@ def test_many_sequences():
                  new_lens=new_lens, status=st)
     mk.check_status(st)
     assert torch.equal(pg.v.cpu(), want) and new_lens.tolist() == [a + len(p) for a, p in zip(ctx, paths)]
+
+
+RUN_POSITIONS = {
+    "repeated": lambda n: [0 if j < 7 * n // 10 else j for j in range(n)],
+    "permuted": lambda n: [7 * j % n for j in range(n)],
+    "reversed": lambda n: [n - 1 - j for j in range(n)],
+    "blocks": lambda n: [(j + 300) % n for j in range(n)],
+}
+
+
+@pytest.mark.parametrize("order", list(RUN_POSITIONS))
+@pytest.mark.parametrize("n_q,n_kv,d,P,ctx,new,window", [
+    (2, 2, 64, 16, [0], [1000], 900), (8, 1, 128, 64, [0, 77], [1000, 501], 500), (8, 2, 64, 64, [300], [640], 128),
+    (1, 1, 128, 32, [2000], [600], 599), (1, 1, 64, 16, [130], [600], 600)])
+def test_attn_run_with_positions_and_a_window(n_q, n_kv, d, P, ctx, new, window, order):
+    """A run whose positions are not its slots: new tokens can be a window apart in either order, so whole tiles of them are
+    seen by some rows of a group only (not where the window holds all of them: the last two shapes)."""
+    assert all(math.gcd(7, n) == 1 for n in new)
+    g = gen(91)
+    pg = Paged(g, [a + b for a, b in zip(ctx, new)], n_kv, P, d)
+    q = torch.randn(sum(new), n_q, d, generator=g, device=DEV).to(BF)
+    pos = [[c + p for p in RUN_POSITIONS[order](n)] for c, n in zip(ctx, new)]
+    st = new_status()
+    out, lse = run_attn(pg, q, ctx, new, window=window, positions=ints([p for row in pos for p in row]), status=st)
+    mk.check_status(st)
+    check_attn(pg, q, out, lse, pg.tables, ctx, new, None, pos, window, 1 / math.sqrt(d), n_kv)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attn_run_with_positions_leaves_values_outside_the_window_out(value):
+    g = gen(92)
+    n, W, P, d = 700, 450, 16, 64
+    pg = Paged(g, [n], 1, P, d)
+    q = torch.randn(n, 2, d, generator=g, device=DEV).to(BF)
+    pos = RUN_POSITIONS["permuted"](n - 1) + [n - 1]
+    kw = dict(window=W, positions=ints(pos))
+    clean, clean_lse = run_attn(pg, q, [0], [n], **kw)
+    j = 300
+    page = pg.tables[0, j // P].item()
+    pg.v[0, page, :, j % P] = value
+    pg.k[0, page, :, j % P, 3] = value
+    out, lse = run_attn(pg, q, [0], [n], **kw)
+    see = torch.tensor([j <= i and pos[i] - pos[j] < W for i in range(n)], device=DEV)
+    assert torch.equal(out[~see], clean[~see]) and torch.equal(lse[~see], clean_lse[~see])
+    if math.isnan(value):
+        assert out[see].isnan().all()
