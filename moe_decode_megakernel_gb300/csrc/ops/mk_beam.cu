@@ -90,7 +90,7 @@ struct Parts {
   uint64_t list[kWarps * Best<N>::kFull + 8];
   float top[kThreads];  // the groups' maxima
   int count;
-  uint32_t least;  // the n-th largest of them, ordered
+  uint32_t least[2];  // the n-th largest of them, ordered, by turns
   uint32_t bound;  // the best bound of any warp, ordered
 };
 
@@ -136,15 +136,16 @@ __device__ __forceinline__ uint64_t keep_best(Best<N>& k, int count, int n) {
 // The n-th largest of the maxima of the block's groups of threads, ordered: at
 // least n of the logits seen so far reach it.  64 groups for n_out up to 32,
 // 256 beyond: of 4096 random logits few more than n reach it (the n-th best of
-// a warp's 512 would let eight times as many pass).
+// a warp's 512 would let eight times as many pass).  The calls take turns (0, 1,
+// 0, ...): a warp may still read one call's result while another begins the next.
 template <int N>
-__device__ __forceinline__ uint32_t bound_of(Parts<N>& sh, float t, int n) {
+__device__ __forceinline__ uint32_t bound_of(Parts<N>& sh, float t, int n, int turn) {
   constexpr int kLanes = N == 32 ? 4 : 1, kGroups = kThreads / kLanes;
   const int tid = threadIdx.x;
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) t = fmaxf(t, __shfl_xor_sync(FULL, t, o));
   if (tid % kLanes == 0) sh.top[tid / kLanes] = t;
-  if (tid == 0) sh.least = 0xffffffffu;
+  if (tid == 0) sh.least[turn] = 0xffffffffu;
   __syncthreads();
   if (tid < kGroups) {
     const float mine = sh.top[tid];
@@ -155,10 +156,10 @@ __device__ __forceinline__ uint32_t bound_of(Parts<N>& sh, float t, int n) {
       above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
     }
     const uint32_t least = __reduce_min_sync(FULL, above < n ? ordered(mine) : 0xffffffffu);
-    if (tid % 32 == 0) atomicMin(&sh.least, least);
+    if (tid % 32 == 0) atomicMin(&sh.least[turn], least);
   }
   __syncthreads();
-  return sh.least;
+  return sh.least[turn];
 }
 
 template <int N>
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
     const int tile = (base - lo) / kTile;
     bool all = false;
     if ((tile & (tile + 1)) == 0 && (tile == 0 || base + kTile < hi)) {
-      const uint32_t o = bound_of(sh, m, n);
+      const uint32_t o = bound_of(sh, m, n, __popc(tile) & 1);
       if (o > ordered(-INFINITY)) {
         if (tid == 0) atomicMax(&sh.bound, o);
         least = fmaxf(least, just_below(o));
@@ -446,9 +447,10 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
     sort_out(k, n);
   }
   for (int i = tid; i < n; i += kThreads) {
-    const uint32_t c = ~k.index[i];
+    const bool there = i < k.count;  // it is, unless an input changed between the kernels
+    const uint32_t c = there ? ~k.index[i] : 0;
     const int64_t o = (int64_t)r * n + i;
-    a.out_scores[o] = (float)unordered64(k.score[i]);
+    a.out_scores[o] = there ? (float)unordered64(k.score[i]) : -INFINITY;
     a.out_parents[o] = (int32_t)(c / (uint32_t)a.vocab);
     a.out_tokens[o] = (int32_t)(c % (uint32_t)a.vocab);
   }

@@ -1097,3 +1097,24 @@ def test_attn_run_with_positions_leaves_values_outside_the_window_out(value):
     assert torch.equal(out[~see], clean[~see]) and torch.equal(lse[~see], clean_lse[~see])
     if math.isnan(value):
         assert out[see].isnan().all()
+
+
+@pytest.mark.parametrize("first,later,n", [(5, 0, 16), (3, 8, 16), (0, 9, 16), (0, 200, 16), (12, 3000, 16), (90, 20, 128), (40, 500, 128)])
+def test_select_masked_vocabulary_over_several_tiles(first, later, n):
+    """Enough rows that a block takes all tiles of one: fewer than n allowed tokens in its first tile, so that no bound holds
+    there, and few or many behind it."""
+    g = gen(94)
+    R, W, V = 83, 4, 20000
+    logits = torch.full((R, W, V), -math.inf, device=DEV)
+    for lo, hi, count in ((0, 4096, first), (4096, V, later)):
+        if count:
+            at = torch.randint(lo, hi, (R, W, count), generator=g, device=DEV)
+            logits.scatter_(2, at, torch.randn(R, W, count, generator=g, device=DEV))
+    scores = -torch.rand(R, W, generator=g, device=DEV)
+    got = run_select(logits, scores, n)
+    check_select(got, logits, scores, n)
+    best, beam, token = plain.select(logits.cpu(), scores.cpu(), n)
+    dead = best[:, :n] == -math.inf  # in the order of the indices
+    assert torch.equal(got[1].cpu().long()[dead], beam[dead]) and torch.equal(got[2].cpu().long()[dead], token[dead])
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(got, run_select(logits, scores, n)))
