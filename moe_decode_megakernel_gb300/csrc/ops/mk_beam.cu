@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, N == 32 ? 4 : 3) select_parts(const 
       }
     }
     __syncwarp();
-    count = *reinterpret_cast<volatile int*>(&k.count);
+    // one lane's reading for all: one that came late could see the next tile's candidates
+    count = __shfl_sync(FULL, *reinterpret_cast<volatile int*>(&k.count), 0);
     if (count > Best<N>::kFull || (!bounded && count >= n)) {
       const uint32_t o = (uint32_t)(keep_best(k, count, n) >> 32);
       count = n;
