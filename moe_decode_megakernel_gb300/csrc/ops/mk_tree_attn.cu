@@ -717,7 +717,9 @@ __device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int
 }
 
 // Q of an item: 16-byte chunks of its rows, first into registers, then into the
-// MMA's K-major layout.
+// MMA's K-major layout.  By ordinary loads: the kernel before this one may have
+// written Q while this one was resident already, and read-only loads hold for
+// data that no one writes as long as a kernel lives.
 template <int D>
 struct QTile {
   static constexpr int kChunks = kRows * (D / 8) / 256;  // of a thread
@@ -732,7 +734,7 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, QTile<
     q.u[x] = make_uint4(0, 0, 0, 0);
     if (x < n && row < it.rows) {
       const uint32_t f = it.row0 + row, i = f / (uint32_t)a.group, g = f % (uint32_t)a.group;
-      q.u[x] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D) + ch);
+      q.u[x] = reinterpret_cast<const uint4*>(a.q + (int64_t)(it.t0 + i) * a.q_stride + (int64_t)(it.h * a.group + g) * D)[ch];
     }
   }
 }

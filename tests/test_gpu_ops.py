@@ -1118,3 +1118,29 @@ def test_select_masked_vocabulary_over_several_tiles(first, later, n):
     assert torch.equal(got[1].cpu().long()[dead], beam[dead]) and torch.equal(got[2].cpu().long()[dead], token[dead])
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(got, run_select(logits, scores, n)))
+
+
+def test_attention_right_behind_an_append_in_place():
+    """Q rotated onto itself (rows that share cache lines with their neighbours) and read by the next kernel, which is let in
+    before the append has ended; with and without a wait between the calls."""
+    g = gen(95)
+    n_q, n_kv, d, P, n = 5, 1, 64, 16, 900
+    pg = Paged(g, [n + 40], n_kv, P, d)
+    src = torch.randn(n, (n_q + 2 * n_kv) * d + 24, generator=g, device=DEV).to(BF)
+    cu, cl = ints([0, n]), ints([40])
+    ws = torch.empty(mk.tree_attn_workspace_bytes(pg.cache), dtype=torch.uint8, device=DEV)
+
+    def run(wait):
+        rows = src.clone()
+        x = rows[:, :(n_q + 2 * n_kv) * d].unflatten(1, (-1, d))
+        out = torch.empty(n, n_q, d, dtype=BF, device=DEV)
+        torch.cuda.synchronize()
+        mk.kv_append(pg.cache, 0, x[:, n_q:n_q + 1], x[:, n_q + 1:], cu, cl, pg.tables, q=x[:, :n_q], q_out=x[:, :n_q])
+        if wait:
+            torch.cuda.synchronize()
+        mk.tree_attn(pg.cache, 0, x[:, :n_q], out, cu, cl, pg.tables, ws)
+        return x[:, :n_q].clone(), out
+    q, want = run(True)
+    for _ in range(30):
+        again = run(False)
+        assert torch.equal(again[0], q) and torch.equal(again[1], want)
