@@ -402,12 +402,12 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       const double cum = scores[w];
       double score = -INFINITY;
       int token;
-      if (done[w]) {
+      if (done[w] && scores[w] > -INFINITY) {
         // its one continuation, then the rest of the vocabulary at -inf
         token = j == 0 ? a.eos : j - 1 + (j - 1 >= a.eos);
         if (j >= n || token >= a.vocab) continue;
         if (j == 0) score = cum;
-      } else if (lse[w] != lse[w]) {
+      } else if (done[w] || lse[w] != lse[w]) {  // all at -inf
         token = j;
         if (j >= n || token >= a.vocab) continue;
       } else {

@@ -1144,3 +1144,18 @@ def test_attention_right_behind_an_append_in_place():
     for _ in range(30):
         again = run(False)
         assert torch.equal(again[0], q) and torch.equal(again[1], want)
+
+
+@pytest.mark.parametrize("score", [-math.inf, math.nan])
+@pytest.mark.parametrize("eos", [0, 2, 5, 39])
+def test_select_finished_beams_without_a_score(score, eos):
+    """A finished beam whose score is -inf (or no number) has no better continuation than any other: the lowest indices."""
+    logits = torch.randn(1, 2, 40, generator=gen(51), device=DEV)
+    fin = torch.ones(1, 2, dtype=torch.uint8, device=DEV)
+    scores = torch.tensor([[score, -2.0]], device=DEV)
+    got = run_select(logits, scores, 6, fin, eos)
+    # the living score first, then 0, 1, 2, ... of beam 0
+    assert got[0].tolist() == [[-2.0] + [-math.inf] * 5]
+    assert got[1].tolist() == [[1] + [0] * 5] and got[2].tolist() == [[eos, 0, 1, 2, 3, 4]]
+    got = run_select(logits[:, :1].contiguous(), scores[:, :1].contiguous(), 6, fin[:, :1].contiguous(), eos)
+    assert got[0].tolist() == [[-math.inf] * 6] and got[2].tolist() == [[0, 1, 2, 3, 4, 5]]
