@@ -3,10 +3,12 @@
 //
 // Two kernels.  The first reads the logits once: blocks (row, part) keep the
 // running maximum and sum of exponentials of their part of a row beside its
-// n_out largest logits (within a beam the order of the scores is that of the
-// logits, so nothing else of the part can be chosen).  The second, a block per
-// request, joins the parts' sums in 64 bits, forms the scores of what is left
-// and takes the best n_out.
+// n_out largest logits (within a beam no score is above that of a larger logit,
+// so nothing else of the part can be better).  The second, a block per request,
+// joins the parts' sums in 64 bits, forms the scores of what is left and takes
+// the best n_out.  Different logits can round to one score, where the lower
+// index comes first: if that may concern the last place, the request's logits
+// are gone through once more (lowest_ties).
 //
 // Measured on a GB300: 64 requests of 8 beams over 65536 tokens (134 MB), the
 // best 16, 37 us: the first kernel 28 (4.8 TB/s, bound by its instructions:
@@ -38,8 +40,9 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t o) {
   return o == 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
-// The largest number below the one ordered as o (-0 has no code of its own).
+// The next numbers below and above the one ordered as o (-0 has no code of its own).
 __device__ __forceinline__ float just_below(uint32_t o) { return unordered(o - (o == 0x80000000u ? 2 : 1)); }
+__device__ __forceinline__ float just_above(uint32_t o) { return unordered(o + 1); }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return (uint64_t)ordered(x) << 32 | (uint32_t)~index; }
 
 struct Key2 {  // a score in 64 bits and the candidate's index
@@ -342,6 +345,53 @@ __device__ __forceinline__ void sort_out(Joined& k, int n) {
   __syncthreads();
 }
 
+// Gives the places of the last one's score to the lowest indices of all
+// continuations that score the same (by the whole block; all that score higher
+// are among the n, so the scores stay).  score(w, x): of logit x in beam w, top:
+// the beams' largest logits.  Only for scores above -inf, so beams without a
+// log-sum-exp have none.  It takes logits that differ by less than the last bit
+// of their score, 2^-52 of it: not made fast.
+template <typename F>
+__device__ __noinline__ void lowest_ties(const SelectArgs& a, Joined& k, const bool* done, const float* scores,
+                                         const double* lse, const float* top, F score) {
+  __shared__ int found[kWarps];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = a.n_out;
+  const uint64_t last = k.score[n - 1];
+  int at = 0;
+  while (k.score[at] > last) ++at;
+  for (int w = 0; w < a.beams && at < n; ++w) {
+    if (done[w]) {
+      if (ordered64(scores[w]) == last) {
+        if (tid == 0) k.index[at] = ~(uint32_t)(w * a.vocab + a.eos);
+        ++at;
+      }
+      continue;
+    }
+    if (lse[w] != lse[w] || ordered64(score(w, top[w])) < last) continue;
+    const float* x = a.logits + ((int64_t)blockIdx.x * a.beams + w) * a.stride;
+    for (int v0 = 0; v0 < a.vocab && at < n; v0 += kTile) {
+      uint32_t hit = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int v = v0 + i * kThreads + tid;
+        if (v < a.vocab && ordered64(score(w, x[v])) == last) hit |= 1u << i;
+      }
+      if (!__syncthreads_or(hit)) continue;
+      for (int i = 0; i < kPer && at < n; ++i) {
+        const uint32_t in = __ballot_sync(FULL, hit >> i & 1);
+        if (lane == 0) found[warp] = __popc(in);
+        __syncthreads();
+        int mine = at + __popc(in & ((1u << lane) - 1));
+        for (int x = 0; x < warp; ++x) mine += found[x];
+        if ((hit >> i & 1) && mine < n) k.index[mine] = ~(uint32_t)(w * a.vocab + v0 + i * kThreads + tid);
+        for (int x = 0; x < kWarps; ++x) at += found[x];
+        __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint4 raw[];
   Joined& k = *reinterpret_cast<Joined*>(raw);
@@ -391,6 +441,11 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
     lse[w] = isfinite(l) && scores[w] > -INFINITY ? l : NAN;
   }
   __syncthreads();
+  auto score_of = [&](int w, float x) {
+    const double s = (double)scores[w] + ((double)x - lse[w]);
+    return s != s ? -INFINITY : s;
+  };
+  uint64_t tied = 0;  // the best score of a part's last kept logit that a neighbouring logit would have too
   for (int base = 0; base < N; base += kTile) {
     Key2 key[kPer], b = {0, 0};
 #pragma unroll
@@ -399,14 +454,13 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       key[i] = {0, 0};
       if (c >= N) continue;
       const int w = c / per_row, j = c % per_row;
-      const double cum = scores[w];
       double score = -INFINITY;
       int token;
       if (done[w] && scores[w] > -INFINITY) {
         // its one continuation, then the rest of the vocabulary at -inf
         token = j == 0 ? a.eos : j - 1 + (j - 1 >= a.eos);
         if (j >= n || token >= a.vocab) continue;
-        if (j == 0) score = cum;
+        if (j == 0) score = scores[w];
       } else if (done[w] || lse[w] != lse[w]) {  // all at -inf
         token = j;
         if (j >= n || token >= a.vocab) continue;
@@ -414,9 +468,17 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
         const uint64_t q = base == 0 && i == 0 ? early : keys[c];
         if (q == 0) continue;
         token = (int)~(uint32_t)q;
-        score = cum + ((double)unordered((uint32_t)(q >> 32)) - lse[w]);
+        const uint32_t o = (uint32_t)(q >> 32);
+        score = score_of(w, unordered(o));
+        // Of a part of more than n logits no other one scores above its last kept
+        // one, and one that scores the same is of no account unless that is the
+        // last place's score and either of them has another logit.
+        if ((j + 1) % n == 0 && o > ordered(-INFINITY) &&
+            (score_of(w, just_below(o)) == score || score_of(w, just_above(o)) == score)) {
+          const uint64_t t = ordered64(score);
+          if (t > tied) tied = t;
+        }
       }
-      if (score != score) score = -INFINITY;
       key[i] = {ordered64(score), ~(uint32_t)(w * a.vocab + token)};
       if (above(key[i], b)) b = key[i];
     }
@@ -447,6 +509,8 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       }
     sort_out(k, n);
   }
+  if (__syncthreads_or(tied != 0 && k.count == n && tied == k.score[n - 1]))
+    lowest_ties(a, k, done, scores, lse, top, score_of);
   for (int i = tid; i < n; i += kThreads) {
     const bool there = i < k.count;  // it is, unless an input changed between the kernels
     const uint32_t c = there ? ~k.index[i] : 0;

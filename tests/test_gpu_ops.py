@@ -1159,3 +1159,83 @@ def test_select_finished_beams_without_a_score(score, eos):
     assert got[1].tolist() == [[1] + [0] * 5] and got[2].tolist() == [[eos, 0, 1, 2, 3, 4]]
     got = run_select(logits[:, :1].contiguous(), scores[:, :1].contiguous(), 6, fin[:, :1].contiguous(), eos)
     assert got[0].tolist() == [[-math.inf] * 6] and got[2].tolist() == [[0, 1, 2, 3, 4, 5]]
+
+
+@pytest.mark.parametrize("R,W,V,n", [(1, 4, 1000, 6), (2, 3, 4096, 128), (1, 2, 9000, 16), (1, 64, 40, 33)])
+@pytest.mark.parametrize("low", [-1e30, -3.4028234663852886e38])
+def test_select_scores_that_absorb_the_logits(R, W, V, n, low):
+    """A beam's score so far from zero that all its continuations score the same in 64 bits: the lowest tokens, not the
+    largest logits."""
+    g = gen(47)
+    logits = torch.randn(R, W, V, generator=g, device=DEV) * 3
+    for lows in (range(W), range(1, W), [w for w in range(W) if w % 2]):
+        scores = -torch.rand(R, W, generator=g, device=DEV)
+        scores[:, list(lows)] = low
+        x = logits.clone()
+        if 0 not in lows:  # the other beams have few continuations, so that the absorbed ones are wanted
+            for w in set(range(W)) - set(lows):
+                x[:, w, 3:] = -math.inf
+        got = run_select(x, scores, n)
+        best, beam, token = plain.select(x.cpu(), scores.cpu(), n)
+        assert torch.equal(got[1].cpu().long(), beam) and torch.equal(got[2].cpu().long(), token)
+        check_select(got, x, scores, n)
+
+
+def test_select_logits_below_the_last_bit_of_the_score():
+    g = gen(48)
+    # all logits far below the last bit of their log-sum-exp: every score of a beam is the same
+    logits = torch.randn(1, 2, 9000, generator=g, device=DEV) * 1e-30
+    scores = torch.tensor([[-1.0, -0.5]], device=DEV)
+    for n in (1, 7, 128):
+        got = run_select(logits, scores, n)
+        assert got[1].tolist() == [[1] * n] and got[2].tolist() == [list(range(n))]
+
+
+@pytest.mark.parametrize("n", [3, 8, 16, 40])
+def test_select_ties_of_different_logits(n):
+    """Two groups of logits that differ by less than the scores' last bit within a group: a tie at the border is broken by
+    the index, across beams, and what lies above it is kept."""
+    V, W, a = 6000, 3, 5
+    r = torch.Generator().manual_seed(49)
+    logits, groups = torch.rand(1, W, V, generator=r) * 1e-7, []
+    for w in range(W):
+        at = torch.randperm(V, generator=r)[:a].sort().values
+        logits[0, w, at] = 1 + torch.arange(a).flip(0) * 2.0 ** -22
+        groups.append(at.tolist())
+    scores = torch.full((1, W), -1e12)
+    # the groups hold together and apart, whatever the last bits of the log-sum-exp
+    cand = scores.double()[..., None] + (logits.double() - torch.logsumexp(logits.double(), -1, keepdim=True))
+    for shift in (-2.0 ** -20, 2.0 ** -20):
+        moved = scores.double()[..., None] + (logits.double() - torch.logsumexp(logits.double(), -1, keepdim=True) + shift)
+        assert torch.equal(cand, moved) and len(cand.unique()) == 2
+    got = run_select(logits.to(DEV), scores.to(DEV), n)
+    top = [(w, t) for w in range(W) for t in groups[w]]
+    rest = [(0, t) for t in range(V) if t not in groups[0]]
+    want = (top + rest)[:n]
+    assert list(zip(got[1][0].tolist(), got[2][0].tolist())) == want
+
+
+def test_select_infinite_score():
+    """A beam of score +inf: all its finite continuations are worth the same."""
+    logits = torch.randn(1, 2, 500, generator=gen(50), device=DEV)
+    logits[0, 1, :4] = -math.inf
+    got = run_select(logits, torch.tensor([[-1.0, math.inf]], device=DEV), 6)
+    assert got[0].tolist() == [[math.inf] * 6] and got[1].tolist() == [[1] * 6] and got[2].tolist() == [[4, 5, 6, 7, 8, 9]]
+
+
+def test_select_absorbed_scores_beside_finished_beams_and_in_long_rows():
+    g = gen(52)
+    # a finished beam of the same score as the absorbed ones around it
+    logits = torch.randn(2, 4, 300, generator=g, device=DEV)
+    scores = torch.full((2, 4), -1e30, device=DEV)
+    scores[1, 0] = -2e30
+    fin = torch.tensor([[1, 0, 1, 0], [0, 1, 0, 0]], dtype=torch.uint8, device=DEV)
+    got = run_select(logits, scores, 5, fin, 7)
+    assert got[1].tolist() == [[0, 1, 1, 1, 1], [1, 2, 2, 2, 2]] and got[2].tolist() == [[7, 0, 1, 2, 3]] * 2
+    # several tiles to a part, ties behind many tiles without any
+    R, W, V, n = 83, 4, 13000, 16
+    logits = torch.full((R, W, V), -math.inf, device=DEV)
+    logits[:, :, 12000:] = torch.randn(R, W, 1000, generator=g, device=DEV)
+    scores = torch.full((R, W), -3e38, device=DEV)
+    got = run_select(logits, scores, n)
+    assert (got[1] == 0).all() and (got[2] == torch.arange(12000, 12000 + n, device=DEV, dtype=torch.int32)).all()
