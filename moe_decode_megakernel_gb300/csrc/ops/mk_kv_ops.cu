@@ -193,9 +193,10 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
         record(a.status, dev::ERR_INDEX, OP_COMMIT, b, k, s, (uint32_t)slots);
       } else {
         const int page = table[(ctx + s) >> a.pools.page_shift], dst = table[(ctx + k) >> a.pools.page_shift];
-        if (page < 0 || page >= a.pools.num_pages || dst < 0 || dst >= a.pools.num_pages) {
+        const bool from_bad = page < 0 || page >= a.pools.num_pages;
+        if (from_bad || dst < 0 || dst >= a.pools.num_pages) {
           bad = true;
-          record(a.status, dev::ERR_PAGE, OP_COMMIT, b, k, page, (uint32_t)a.pools.num_pages);
+          record(a.status, dev::ERR_PAGE, OP_COMMIT, b, k, from_bad ? page : dst, (uint32_t)a.pools.num_pages);
         }
         if (k < kRound) {
           from[k] = s == k ? -1 : row_of(page, ctx + s);
@@ -321,8 +322,9 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
   for (int u = blockIdx.y; u < units * n_copy; u += gridDim.y) {
     const int e = u / units, w = u % units;
     const int layer = w / (2 * a.pools.n_kv), h = w % a.pools.n_kv;
-    if (src[e] < 0 || src[e] >= a.pools.num_pages || dst[e] < 0 || dst[e] >= a.pools.num_pages) {
-      if (tid == 0) record(a.status, dev::ERR_PAGE, OP_REORDER, r, e, src[e], (uint32_t)a.pools.num_pages);
+    const bool from_bad = src[e] < 0 || src[e] >= a.pools.num_pages;
+    if (from_bad || dst[e] < 0 || dst[e] >= a.pools.num_pages) {
+      if (tid == 0) record(a.status, dev::ERR_PAGE, OP_REORDER, r, e, from_bad ? src[e] : dst[e], (uint32_t)a.pools.num_pages);
       continue;
     }
     uint4* pool = reinterpret_cast<uint4*>((w / a.pools.n_kv % 2 ? a.pools.v : a.pools.k) + layer * a.pools.layer_elems);

@@ -1239,3 +1239,23 @@ def test_select_absorbed_scores_beside_finished_beams_and_in_long_rows():
     scores = torch.full((R, W), -3e38, device=DEV)
     got = run_select(logits, scores, n)
     assert (got[1] == 0).all() and (got[2] == torch.arange(12000, 12000 + n, device=DEV, dtype=torch.int32)).all()
+
+
+def test_records_name_the_page_that_is_out_of_range():
+    """A good source and a bad destination, and the other way round: the message has the bad one."""
+    P = 16
+    pg = Paged(gen(93), [32, 32], 1, P, 64, extra_cols=0)
+    for column, slot_from, bad in ((0, 3, 54321), (1, 3, 54321), (0, 3, -17)):
+        tables, st = pg.tables.clone(), new_status()
+        tables[0, column] = bad
+        mk.kv_commit(pg.cache, ints([14, 14]), ints([[slot_from], [slot_from]]), ints([1, 1]), tables, status=st)  # 17 -> 14
+        with pytest.raises(mk.MkError) as e:
+            mk.check_status(st)
+        assert f"page id {bad} out of range" in str(e.value)
+    for row, bad in ((0, 54321), (1, 54321), (1, -17)):  # beam 0 survives, beam 1's open page takes the copy
+        tables, st = pg.tables.clone(), new_status()
+        tables[row, 1] = bad
+        mk.beam_reorder(pg.cache, ints([20]), ints([[0, 0]]), tables, torch.empty_like(tables), status=st)
+        with pytest.raises(mk.MkError) as e:
+            mk.check_status(st)
+        assert f"page id {bad} out of range" in str(e.value)
