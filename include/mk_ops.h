@@ -160,7 +160,7 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
  *  new_lens   device int32 [batch], receives cache_lens[b] + path_lens[b];
  *             apart from the inputs; or NULL
  * A sequence whose path does not ascend, is longer than max_path or leaves
- * its pages is left out (its new length is its cache length). */
+ * its pages is left out (its new length is its cache length).  batch <= 65535. */
 int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, const int32_t* path,
                  const int32_t* path_lens, int32_t max_path, const int32_t* block_tables,
                  int32_t max_pages, int32_t* new_lens, uint32_t* status, void* stream);
@@ -178,8 +178,9 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
  *  finished   device uint8 [requests][beams], nonzero: finished; or NULL
  *  out_*      device [requests][n_out]: scores fp32, parent beams int32,
  *             tokens int32; apart from the inputs
- * beams <= 64, n_out <= 128, n_out <= beams * vocab <= 2^30; with finished,
- * 0 <= eos < vocab. */
+ * beams <= 64, n_out <= 128, n_out <= beams * vocab <= 2^30, requests * beams
+ * <= 65535; with finished, 0 <= eos < vocab.  Bytes of workspace (16-byte
+ * aligned): 0 for a shape that the call refuses. */
 size_t mk_beam_select_workspace_bytes(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out);
 int mk_beam_select(const float* logits, int64_t logits_stride, const float* scores,
                    const uint8_t* finished, int32_t eos, int32_t requests, int32_t beams,

@@ -535,10 +535,11 @@ int parts_of(int64_t rows, int vocab) {
   return (int)((tiles + per - 1) / per);
 }
 
-// The kernels count a row's logits in 32 bits, up to two tiles behind its end.
+// The kernels count a row's logits in 32 bits, up to two tiles behind its end;
+// the rows are a grid's second dimension.
 bool shape_ok(int32_t requests, int32_t beams, int32_t vocab, int32_t n_out) {
   return requests >= 0 && beams >= 1 && beams <= kMaxBeams && vocab >= 1 && n_out >= 1 && n_out <= kMaxOut &&
-         n_out <= (int64_t)beams * vocab && (int64_t)beams * vocab <= 1 << 30 && requests <= 1 << 20;
+         n_out <= (int64_t)beams * vocab && (int64_t)beams * vocab <= 1 << 30 && (int64_t)requests * beams <= 65535;
 }
 
 size_t sums_bytes(int64_t rows, int parts) { return (size_t)rows * parts * sizeof(double2); }
@@ -563,7 +564,7 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
                    int32_t eos, int32_t requests, int32_t beams, int32_t vocab, int32_t n_out, float* out_scores,
                    int32_t* out_parents, int32_t* out_tokens, void* workspace, size_t workspace_bytes, void* stream) {
   if (!shape_ok(requests, beams, vocab, n_out))
-    return fail(MK_ERR_ARG, "beams 1 to 64, n_out 1 to 128 and at most beams * vocab (up to 2^30)");
+    return fail(MK_ERR_ARG, "beams 1 to 64, n_out 1 to 128 and at most beams * vocab (up to 2^30), requests * beams up to 65535");
   if (requests == 0) return MK_OK;
   if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return fail(MK_ERR_ARG, "null argument");
   if (misplaced(logits, scores, finished, out_scores, out_parents, out_tokens)) return fail(MK_ERR_ARG, "misaligned argument");
@@ -594,7 +595,6 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
   a.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows, a.parts));
   a.vec = !misaligned(logits) && logits_stride % 4 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (rows > 65535) return fail(MK_ERR_ARG, "more than 65535 rows of logits");
   constexpr int smem = (int)sizeof(Joined);
   static std::atomic<uint64_t> join_ready{0}, wide_ready{0};
   int rc = allow_smem(join_ready, reinterpret_cast<const void*>(&select_join), smem, "select");

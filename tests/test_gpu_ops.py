@@ -1259,3 +1259,11 @@ def test_records_name_the_page_that_is_out_of_range():
         with pytest.raises(mk.MkError) as e:
             mk.check_status(st)
         assert f"page id {bad} out of range" in str(e.value)
+
+
+def test_select_as_many_rows_as_it_takes():
+    g = gen(96)
+    R, W, V, n = 16383, 4, 20, 4
+    logits = torch.randn(R, W, V, generator=g, device=DEV) * 3
+    scores = -10 * torch.rand(R, W, generator=g, device=DEV)
+    check_select(run_select(logits, scores, n), logits, scores, n)

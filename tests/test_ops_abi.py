@@ -283,3 +283,12 @@ def test_binding_refuses_what_ctypes_would_take():
     assert not refused(mk.beam_select, **select)
     assert refused(mk.beam_select, **select, eos=1 << 32)
     assert refused(mk.beam_select, **{**select, "logits": torch.zeros(1).expand(1 << 33).unflatten(0, (2, 1 << 32))})
+
+
+@pytest.mark.parametrize("requests,beams", [(65536, 1), (1024, 64), (1 << 20, 2), (16384, 4)])
+def test_select_sizes_no_workspace_for_rows_that_it_refuses(requests, beams):
+    a = dict(SELECT, requests=requests, beams=beams, vocab=16, stride=16, logits=1 << 44, scores=1 << 43, finished=None,
+             out_scores=1 << 42, out_parents=3 << 41, out_tokens=5 << 40, bytes=1 << 36)
+    assert ops._lib().mk_beam_select(*a.values(), None) == mk.MK_ERR_ARG
+    assert mk.beam_select_workspace_bytes(requests, beams, 16, 8) == 0
+    assert mk.beam_select_workspace_bytes(65535 // beams, beams, 16, 8) > 0
