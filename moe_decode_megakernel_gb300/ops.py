@@ -252,7 +252,10 @@ def kv_commit(cache: KvCache, cache_lens, path, path_lens, block_tables, new_len
 
 def beam_select_workspace_bytes(requests: int, beams: int, vocab: int, n_out: int) -> int:
     """mk_beam_select_workspace_bytes (0: a shape that beam_select refuses)."""
-    return int(_lib().mk_beam_select_workspace_bytes(requests, beams, vocab, n_out))
+    shape = (requests, beams, vocab, n_out)
+    if any(not 0 <= x < 1 << 31 for x in shape):  # ctypes would cut them off
+        return 0
+    return int(_lib().mk_beam_select_workspace_bytes(*shape))
 
 
 def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, finished=None, eos: int = -1,
@@ -264,7 +267,8 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace, 
     dev, f32, i32 = logits.device, torch.float32, torch.int32
     if scores.dim() != 2 or logits.dim() != 2 or out_scores.dim() != 2:
         _bad("logits, scores and outputs have two dimensions")
-    (R, W), V, n = scores.shape, _int32(logits.shape[1], "vocab"), out_scores.shape[1]
+    R, W = _int32(scores.shape[0], "requests"), _int32(scores.shape[1], "beams")
+    V, n = _int32(logits.shape[1], "vocab"), _int32(out_scores.shape[1], "outputs")
     if logits.dtype is not f32 or logits.shape[0] != R * W or (V > 1 and logits.stride(1) != 1):
         _bad(f"logits: fp32 [{R * W}][vocab] with the vocabulary side by side is wanted, got {logits.dtype} "
              f"{tuple(logits.shape)} strides {logits.stride()}")
@@ -282,7 +286,8 @@ def beam_reorder(cache: KvCache, lens, parents, tables_in, tables_out, status=No
     dev, i32 = cache.device, torch.int32
     _dims(parents, "parents", 2)
     _dims(tables_in, "tables_in", 2)
-    (R, W), pages = parents.shape, _int32(tables_in.shape[1], "page columns")
+    R, W = _int32(parents.shape[0], "requests"), _int32(parents.shape[1], "beams")
+    pages = _int32(tables_in.shape[1], "page columns")
     args = (R, W, _take(lens, "lens", i32, (R,), dev), _take(parents, "parents", i32, (R, W), dev),
             _take(tables_in, "tables_in", i32, (R * W, pages), dev),
             _take(tables_out, "tables_out", i32, (R * W, pages), dev), pages, _status(status, dev))

@@ -292,3 +292,29 @@ def test_select_sizes_no_workspace_for_rows_that_it_refuses(requests, beams):
     assert ops._lib().mk_beam_select(*a.values(), None) == mk.MK_ERR_ARG
     assert mk.beam_select_workspace_bytes(requests, beams, 16, 8) == 0
     assert mk.beam_select_workspace_bytes(65535 // beams, beams, 16, 8) > 0
+
+
+def test_binding_counts_requests_in_32_bits():
+    """More requests, beams or outputs than the call's integers hold: refused, not cut off (tensors without memory)."""
+    import torch
+    n, i32 = (1 << 32) + 1, dict(dtype=torch.int32, device="meta")
+
+    class Fake:
+        device, n_layers, n_kv, head_dim, handle = torch.device("meta"), 2, 2, 64, None
+
+    def f32(*s):
+        return torch.empty(*s, device="meta")
+
+    def refused(f, *args):
+        with pytest.raises(mk.MkError) as e:
+            f(*args)
+        return "32 bits" in str(e.value)
+    w = torch.empty(64, dtype=torch.uint8, device="meta")
+    for R, W, out in ((n, 1, 1), (0, n, 1), (0, 1, n)):
+        o = [torch.empty(R, out, **i32) for _ in range(2)]
+        assert refused(mk.beam_select, f32(R * W, 4), f32(R, W), f32(R, out), *o, w), (R, W, out)
+    for R, W in ((n, 1), (0, n)):
+        t = torch.empty(R * W, 4, **i32)
+        assert refused(mk.beam_reorder, Fake(), torch.empty(R, **i32), torch.empty(R, W, **i32), t, torch.empty_like(t))
+    for shape in ((n, 1, 16, 4), (1, n, 16, 4), (1, 1, n, 4), (1, 4, 16, n), (-1, 1, 16, 4), (1 - (1 << 32), 1, 16, 4)):
+        assert mk.beam_select_workspace_bytes(*shape) == 0
