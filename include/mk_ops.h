@@ -19,9 +19,11 @@
  * captured into a graph, a bad argument returns MK_ERR_ARG before anything is
  * launched (mk_last_error()).  The tensors, the stream and the current device
  * have to be of one device; an array's address is a multiple of its elements'
- * size.  Workspaces lie apart from all other arguments, need no initialisation
- * and hold nothing between calls; calls (and replays of captured calls) that
- * can overlap in time need a workspace each.
+ * size.  The arrays and workspaces that a call writes lie apart from its other
+ * arguments and from the pools (an overlap is refused, but where q_out is q);
+ * the K, V and Q of an append are none of the pool rows that it writes.
+ * Workspaces need no initialisation and hold nothing between calls; calls (and
+ * replays of captured calls) that can overlap in time need a workspace each.
  *
  * Values in device memory are checked on the device.  A call never reads or
  * writes outside the arrays it was given: what a value out of range would

@@ -461,8 +461,9 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
       return col < q_row || col + kv_row > stride;
     };
     if ((!itself && overlap(io->q_out, out, io->q, span(T, io->q_stride, q_row, elem))) ||
-        collides(io->k, io->k_stride) || collides(io->v, io->v_stride))
-      return fail(MK_ERR_ARG, "q_out overlaps an input");
+        collides(io->k, io->k_stride) || collides(io->v, io->v_stride) || over_batch(tok, io->q_out, out) ||
+        over_pools(kv, status, io->q_out, out))
+      return fail(MK_ERR_ARG, "q_out overlaps another argument or the pools");
   }
   AppendArgs a;
   a.pools = pools_of(kv, layer);
@@ -490,8 +491,9 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
   if (overlap(new_lens, 4 * (size_t)batch, cache_lens, 4 * (size_t)batch) ||
       overlap(new_lens, 4 * (size_t)batch, path_lens, 4 * (size_t)batch) ||
       overlap(new_lens, 4 * (size_t)batch, path, 4 * (size_t)batch * max_path) ||
-      overlap(new_lens, 4 * (size_t)batch, block_tables, 4 * (size_t)batch * max_pages))
-    return fail(MK_ERR_ARG, "new_lens overlaps an input");
+      overlap(new_lens, 4 * (size_t)batch, block_tables, 4 * (size_t)batch * max_pages) ||
+      over_pools(kv, status, new_lens, 4 * (size_t)batch))
+    return fail(MK_ERR_ARG, "new_lens overlaps another argument or the pools");
   CommitArgs a;
   a.pools = pools_of(kv, 0);
   a.ctx = cache_lens, a.path = path, a.path_lens = path_lens, a.tables = block_tables, a.new_lens = new_lens;
@@ -514,8 +516,8 @@ int mk_beam_reorder(const mk_kv* kv, int32_t requests, int32_t beams, const int3
   if (misplaced(lens, parents, tables_in, tables_out, status)) return fail(MK_ERR_ARG, "misaligned argument");
   const size_t bytes = 4 * (size_t)requests * beams * max_pages;
   if (overlap(tables_out, bytes, tables_in, bytes) || overlap(tables_out, bytes, parents, 4 * (size_t)requests * beams) ||
-      overlap(tables_out, bytes, lens, 4 * (size_t)requests))
-    return fail(MK_ERR_ARG, "tables_out overlaps an input");
+      overlap(tables_out, bytes, lens, 4 * (size_t)requests) || over_pools(kv, status, tables_out, bytes))
+    return fail(MK_ERR_ARG, "tables_out overlaps another argument or the pools");
   ReorderArgs a;
   a.pools = pools_of(kv, 0);
   a.lens = lens, a.parents = parents, a.tables_in = tables_in, a.tables_out = tables_out;

@@ -206,6 +206,19 @@ inline int check_tokens(const mk_kv* kv, int32_t layer, const mk_tokens* t) {
   return MK_OK;
 }
 
+// Whether an array that a call writes lies over the pools, the status record or
+// the arrays of the batch.
+inline bool over_pools(const mk_kv* kv, const uint32_t* status, const void* p, size_t bytes) {
+  const mk_kv_config& c = kv->cfg;
+  const size_t pool = (size_t)c.n_layers * c.num_pages * c.n_kv * c.page_size * c.head_dim * 2;
+  return overlap(p, bytes, c.k_pool, pool) || overlap(p, bytes, c.v_pool, pool) || overlap(p, bytes, status, 32);
+}
+inline bool over_batch(const mk_tokens* t, const void* p, size_t bytes) {
+  const size_t b = (size_t)t->batch * 4;
+  return overlap(p, bytes, t->cu_seqlens, b + 4) || overlap(p, bytes, t->cache_lens, b) ||
+         overlap(p, bytes, t->block_tables, b * t->max_pages) || overlap(p, bytes, t->positions, (size_t)t->n_tokens * 4);
+}
+
 inline Batch batch_of(const mk_tokens* t) {
   return {t->cu_seqlens, t->cache_lens, t->block_tables, t->positions, t->batch, t->n_tokens, t->max_pages};
 }

@@ -1273,6 +1273,12 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
       overlap(workspace, workspace_bytes, io->lse, lse_bytes) || overlap(io->lse, lse_bytes, io->out, out_bytes) ||
       overlap(io->lse, lse_bytes, io->q, q_bytes))
     return fail(MK_ERR_ARG, "workspace or lse overlaps another argument");
+  const size_t mask_bytes = (size_t)tok->n_tokens * io->mask_words * 8;
+  auto over_inputs = [&](const void* p, size_t bytes) {
+    return over_batch(tok, p, bytes) || over_pools(kv, status, p, bytes) || overlap(p, bytes, io->tree_mask, mask_bytes);
+  };
+  if (over_inputs(io->out, out_bytes) || over_inputs(io->lse, lse_bytes) || over_inputs(workspace, workspace_bytes))
+    return fail(MK_ERR_ARG, "out, lse or workspace overlaps the batch's arrays, the mask, the status or the pools");
   const int grid = grid_size();
   if (grid < 1) return fail(MK_ERR_CUDA, "no device");
   if (workspace_bytes < part_bytes(grid, c.head_dim)) return fail(MK_ERR_ARG, "workspace smaller than mk_tree_attn_workspace_bytes");

@@ -318,3 +318,25 @@ def test_binding_counts_requests_in_32_bits():
         assert refused(mk.beam_reorder, Fake(), torch.empty(R, **i32), torch.empty(R, W, **i32), t, torch.empty_like(t))
     for shape in ((n, 1, 16, 4), (1, n, 16, 4), (1, 1, n, 4), (1, 4, 16, n), (-1, 1, 16, 4), (1 - (1 << 32), 1, 16, 4)):
         assert mk.beam_select_workspace_bytes(*shape) == 0
+
+
+POOL_K, POOL_V, POOL = 1 << 40, 1 << 41, 2 * 8 * 2 * 16 * 64 * 2  # the fixture's pools
+
+
+@pytest.mark.parametrize("at", [A + 8, 2 * A, 3 * A + 16, 8 * A, POOL_K + POOL - 16, POOL_V, 15 * A], ids=hex)
+def test_outputs_over_the_batch_the_pools_or_the_record(kv, at):
+    L, t = ops._lib(), tokens(positions=8 * A)
+    at16 = at // 16 * 16
+    assert L.mk_kv_append(kv, 0, t, append_io(q_out=at16), 15 * A, None) == mk.MK_ERR_ARG
+    for io, ws in ((attn_io(out=at16), 32 * A), (attn_io(lse=at), 32 * A), (attn_io(), at16)):
+        assert L.mk_tree_attn(kv, 0, t, io, ws, 4096, 15 * A, None) == mk.MK_ERR_ARG
+        assert "overlaps the batch" in mk.last_error()
+    assert L.mk_tree_attn(kv, 0, t, attn_io(lse=6 * A + 16), 32 * A, 4096, 15 * A, None) == mk.MK_ERR_ARG  # the mask
+    assert "overlaps the batch" in mk.last_error()
+
+
+@pytest.mark.parametrize("at", [POOL_K + POOL - 4, POOL_V, 15 * A + 28], ids=hex)
+def test_lengths_and_tables_over_the_pools_or_the_record(kv, at):
+    L = ops._lib()
+    assert L.mk_kv_commit(kv, 2, 2 * A, 3 * A, 4 * A, 4, 5 * A, 4, at, 15 * A, None) == mk.MK_ERR_ARG
+    assert L.mk_beam_reorder(kv, 2, 4, 2 * A, 3 * A, 4 * A, at, 4, 15 * A, None) == mk.MK_ERR_ARG
