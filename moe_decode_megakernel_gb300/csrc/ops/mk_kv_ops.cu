@@ -67,15 +67,17 @@ __device__ __forceinline__ void values(const Chunk<false>& c, float (&x)[8]) {
   }
 }
 
-// One block per token, its heads in 16-byte chunks of output.  The first
-// chunks of every thread are on their way before the token's slot is known
-// (its sequence, then its page: two round trips to memory); the thread whose
-// sequence holds the token looks the slot up, half a head of threads turns the
-// position into sines.  12.6K tokens of 40 heads of 128 (258 MB moved) take 42
+// One block per token (and one for the batch), its heads in 16-byte chunks of
+// output.  The first chunks of every thread are on their way before the token's
+// slot is known (its sequence, then its page: two round trips to memory); the
+// thread whose sequence holds the token looks the slot up, half a head of
+// threads turns the position into sines.  12.6K tokens of 40 heads of 128 (258 MB moved) take 42
 // us, 6.2 TB/s where a copy of that size reaches 6.8: bound by memory.  Small
 // blocks with many chunks of a thread under way: 256 threads with three took 48
 // us, 128 with three 44; 64 with ten were no faster.
-// Eight tokens are a chain of four round trips, about 5 us.
+// Eight tokens are a chain of four round trips, 3 us behind another kernel.  The
+// batch's own block costs nothing beside them; with its check in the first
+// token's block they took 3.3 us, with it in every block the 12.6K tokens 43.
 constexpr int kAppend = 128;
 template <int D, bool F32>
 __global__ void __launch_bounds__(kAppend) append_kernel(const __grid_constant__ AppendArgs a) {
@@ -87,6 +89,13 @@ __global__ void __launch_bounds__(kAppend) append_kernel(const __grid_constant__
   const int t = blockIdx.x, tid = threadIdx.x;
   wait_before();
   let_next_in();
+  if (t == a.b.n_tokens) {  // the batch's block: sequences that may have no token whose block would see what is wrong
+    for (int b = tid; b < a.b.batch; b += kAppend) {
+      const int t0 = a.b.cu[b], t1 = a.b.cu[b + 1];
+      if (t0 < 0 || t1 < t0 || t1 > a.b.n_tokens) record(a.status, dev::ERR_INDEX, OP_APPEND, b, 0, t1, a.b.n_tokens);
+    }
+    return;
+  }
   const int n_kv = a.pools.n_kv, heads = a.n_q + 2 * n_kv, chunks = heads * CPH;
   Chunk<F32> held[kHeld];
   auto load = [&](int base) {
@@ -475,7 +484,7 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
   for (int i = 0; i < 64; ++i) a.freq[i] = kv->freq[i];
   auto kernel = c.head_dim == 128 ? (io->dtype == MK_F32 ? append_kernel<128, true> : append_kernel<128, false>)
                                   : (io->dtype == MK_F32 ? append_kernel<64, true> : append_kernel<64, false>);
-  return launch("append", kernel, dim3((unsigned)T), kAppend, 0, static_cast<cudaStream_t>(stream), a);
+  return launch("append", kernel, dim3((unsigned)T + 1), kAppend, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, const int32_t* path,

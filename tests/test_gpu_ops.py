@@ -1267,3 +1267,14 @@ def test_select_as_many_rows_as_it_takes():
     logits = torch.randn(R, W, V, generator=g, device=DEV) * 3
     scores = -10 * torch.rand(R, W, generator=g, device=DEV)
     check_select(run_select(logits, scores, n), logits, scores, n)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 2, 2], [9, 12, 12, 12], [-7, -2, 0, 3], [0, 9, 9, 8], [3, 3, 3, -1]])
+def test_append_records_sequences_without_a_token(cu):
+    """Lengths below zero and rows that the arrays do not have, where no token belongs to the sequence."""
+    pg = Paged(gen(97), [20] * 3, 2, 16, 64)
+    k, st = torch.ones(9, 2, 64, dtype=BF, device=DEV), new_status()
+    mk.kv_append(pg.cache, 0, k, k, ints(cu), ints([0, 0, 0]), pg.tables, status=st)
+    with pytest.raises(mk.MkError) as e:
+        mk.check_status(st)
+    assert e.value.code == mk.MK_ERR_DEVICE and "kv_append" in str(e.value)
