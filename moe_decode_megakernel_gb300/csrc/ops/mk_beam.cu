@@ -568,7 +568,8 @@ int mk_beam_select(const float* logits, int64_t logits_stride, const float* scor
   if (requests == 0) return MK_OK;
   if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return fail(MK_ERR_ARG, "null argument");
   if (misplaced(logits, scores, finished, out_scores, out_parents, out_tokens)) return fail(MK_ERR_ARG, "misaligned argument");
-  if (logits_stride < vocab) return fail(MK_ERR_ARG, "logits_stride below vocab");
+  if (logits_stride < vocab || endless((int64_t)requests * beams, logits_stride, 4))
+    return fail(MK_ERR_ARG, "logits_stride below vocab, or rows beyond 2^48 bytes");
   if (finished && (eos < 0 || eos >= vocab)) return fail(MK_ERR_ARG, "eos outside the vocabulary");
   if (misaligned(workspace) || !workspace ||
       workspace_bytes < mk_beam_select_workspace_bytes(requests, beams, vocab, n_out))

@@ -418,6 +418,8 @@ int mk_kv_open(const mk_kv_config* cfg, mk_kv** out) {
   if (c.num_pages >= (int64_t)1 << 31 || c.num_pages * c.n_kv >= (int64_t)1 << 31 ||
       c.num_pages * c.n_kv * c.page_size >= (int64_t)1 << 31)
     return fail(MK_ERR_ARG, "2^31 rows or more in a layer of the pools");
+  if (endless(c.n_layers, c.num_pages * c.n_kv * c.page_size * c.head_dim, 2))
+    return fail(MK_ERR_ARG, "pools of more than 2^48 bytes");
   if (!c.k_pool || !c.v_pool || misaligned(c.k_pool) || misaligned(c.v_pool))
     return fail(MK_ERR_ARG, "null or misaligned pool");
   if (!(c.rope_base > 1.0) || !std::isfinite(c.rope_base)) return fail(MK_ERR_ARG, "rope_base must be above 1");
@@ -451,11 +453,11 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
   if (io->n_q < 0 || n_q > (1 << 16)) return fail(MK_ERR_ARG, "bad number of query heads");
   const int64_t kv_row = (int64_t)c.n_kv * c.head_dim, q_row = (int64_t)n_q * c.head_dim;
   auto bad = [&](const void* p, int64_t stride, int64_t row, size_t e) {
-    return misaligned(p) || stride < row || (stride * e) % 16 != 0;
+    return misaligned(p) || stride < row || (stride * e) % 16 != 0 || endless(tok->n_tokens, stride, e);
   };
   if (bad(io->k, io->k_stride, kv_row, elem) || bad(io->v, io->v_stride, kv_row, elem) ||
       (n_q && (bad(io->q, io->q_stride, q_row, elem) || bad(io->q_out, io->q_out_stride, q_row, 2))))
-    return fail(MK_ERR_ARG, "misaligned token array, or a stride that is too small or no multiple of 16 bytes");
+    return fail(MK_ERR_ARG, "misaligned token array, or a stride that is too small, too large or no multiple of 16 bytes");
   const int64_t T = tok->n_tokens;
   if (n_q) {
     // q_out is q itself (k and v may be other columns of the same rows), or

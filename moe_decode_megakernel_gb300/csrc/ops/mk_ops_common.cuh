@@ -136,6 +136,12 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return a && b && an && bn && x < y + bn && y < x + an;
 }
 
+// Whether an array of so many strided rows is longer than addresses reach (2^48
+// bytes), where its offsets would pass 64 bits.
+inline bool endless(int64_t rows, int64_t stride, size_t elem) {
+  return rows > 1 && stride > (int64_t)(((uint64_t)1 << 48) / ((uint64_t)rows * elem));
+}
+
 // Bytes of a strided token array: the last row counts its own elements only.
 inline size_t span(int64_t rows, int64_t stride, int64_t row_elems, size_t elem) {
   return rows > 0 ? (size_t)((rows - 1) * stride + row_elems) * elem : 0;

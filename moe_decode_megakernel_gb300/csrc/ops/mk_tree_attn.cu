@@ -1257,8 +1257,8 @@ int mk_tree_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn_i
   if ((int64_t)tok->n_tokens * (io->n_q / c.n_kv) > INT32_MAX) return fail(MK_ERR_ARG, "more than 2^31 - 1 query rows per K/V head");
   const int64_t row = (int64_t)io->n_q * c.head_dim;
   if (misaligned(io->q) || misaligned(io->out) || io->q_stride < row || io->out_stride < row || io->q_stride % 8 ||
-      io->out_stride % 8)
-    return fail(MK_ERR_ARG, "misaligned q or out, or a stride that is too small or no multiple of 16 bytes");
+      io->out_stride % 8 || endless(tok->n_tokens, io->q_stride, 2) || endless(tok->n_tokens, io->out_stride, 2))
+    return fail(MK_ERR_ARG, "misaligned q or out, or a stride that is too small, too large or no multiple of 16 bytes");
   if (overlap(io->out, span(tok->n_tokens, io->out_stride, row, 2), io->q, span(tok->n_tokens, io->q_stride, row, 2)))
     return fail(MK_ERR_ARG, "out overlaps q");
   if (misplaced(io->tree_mask, io->lse, status)) return fail(MK_ERR_ARG, "misaligned tree_mask, lse or status");

@@ -340,3 +340,22 @@ def test_lengths_and_tables_over_the_pools_or_the_record(kv, at):
     L = ops._lib()
     assert L.mk_kv_commit(kv, 2, 2 * A, 3 * A, 4 * A, 4, 5 * A, 4, at, 15 * A, None) == mk.MK_ERR_ARG
     assert L.mk_beam_reorder(kv, 2, 4, 2 * A, 3 * A, 4 * A, at, 4, 15 * A, None) == mk.MK_ERR_ARG
+
+
+@pytest.mark.parametrize("stride", [1 << 62, (1 << 62) + 256, (1 << 63) - 8, 1 << 48])
+def test_strides_whose_offsets_pass_64_bits(kv, stride):
+    """Arrays longer than addresses reach: offsets would wrap, and the overlaps with them."""
+    L = ops._lib()
+    for bad in (dict(q_stride=stride), dict(k_stride=stride), dict(v_stride=stride), dict(q_out_stride=stride)):
+        assert L.mk_kv_append(kv, 0, tokens(), append_io(**bad), None, None) == mk.MK_ERR_ARG, bad
+        assert "stride" in mk.last_error()
+    for bad in (dict(q_stride=stride), dict(out_stride=stride)):
+        assert L.mk_tree_attn(kv, 0, tokens(), attn_io(**bad), 32 * A, 4096, None, None) == mk.MK_ERR_ARG
+        assert "stride" in mk.last_error()
+    assert L.mk_beam_select(*dict(SELECT, stride=stride).values(), None) == mk.MK_ERR_ARG
+    assert "stride" in mk.last_error()
+
+
+def test_open_refuses_pools_beyond_addresses():
+    rc, h = open_kv(n_layers=(1 << 31) - 1, num_pages=1 << 25)
+    assert rc == mk.MK_ERR_ARG and not h.value
