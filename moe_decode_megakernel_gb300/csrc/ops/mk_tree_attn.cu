@@ -630,6 +630,9 @@ __device__ __forceinline__ bool issue_mmas(const AttnArgs& a, uint8_t* smem, Ctl
   return true;
 }
 
+// Whether one of two bf16 is an infinity or NaN (its exponent all ones).
+__device__ __forceinline__ uint32_t any_odd(uint32_t w) { return ((w & 0x7f80u) == 0x7f80u) | ((w & 0x7f800000u) == 0x7f800000u); }
+
 // Rows of a partly masked tile's V that must not reach the MMA.
 struct CleanState {
   Ring k;
@@ -652,14 +655,11 @@ __device__ bool clean_v(const AttnArgs& a, uint8_t* smem, Ctl& c, CleanState& st
         for (int row = lane; row < kTile; row += 32) {
           bool drop = s0 + row >= len;
           if (!drop && (s0 + row >= it.masked_from || s0 + row < it.window_to)) {
-            uint32_t odd = 0;  // exponents all ones
+            uint32_t odd = 0;
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
               const uint4 u = lds128(tile + ch / 8 * G::kHalfBytes + row * 128 + ((ch % 8) ^ (row & 7)) * 16);
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                odd |= ((w[e] & 0x7f80u) == 0x7f80u) | ((w[e] & 0x7f800000u) == 0x7f800000u);
+              odd |= any_odd(u.x) | any_odd(u.y) | any_odd(u.z) | any_odd(u.w);
             }
             if (odd) {
               drop = true;
@@ -701,15 +701,18 @@ __device__ __forceinline__ void add_odd_v(const AttnArgs& a, const Item& it, int
   for (int j = it.lo; j < it.hi; ++j) {
     if (!in_part(it, j)) continue;
     for (int s = j * kTile; s < min((j + 1) * kTile, it.ctx + it.n); ++s) {
-      if ((s < it.masked_from && s >= it.window_to) || !(seen(a, it, i, pos, word0, s) & 1)) continue;
+      if (s < it.masked_from && s >= it.window_to) continue;
       const int64_t row = pool_row(a, it, s) * D;
-      bool odd = false;
-      float dot = 0;
-      for (int e = 0; e < D; ++e) {
-        odd |= (a.pools.v[row + e] & 0x7f80) == 0x7f80;
-        dot += __uint_as_float((uint32_t)q[e] << 16) * __uint_as_float((uint32_t)a.pools.k[row + e] << 16);
+      uint32_t odd = 0;  // the same for all rows, and quickly known
+#pragma unroll
+      for (int e = 0; e < D; e += 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(a.pools.v + row + e);
+        odd |= any_odd(u.x) | any_odd(u.y) | any_odd(u.z) | any_odd(u.w);
       }
-      if (!odd) continue;
+      if (!odd || !(seen(a, it, i, pos, word0, s) & 1)) continue;
+      float dot = 0;
+      for (int e = 0; e < D; ++e)
+        dot += __uint_as_float((uint32_t)q[e] << 16) * __uint_as_float((uint32_t)a.pools.k[row + e] << 16);
       const float p = ex2(dot * a.scale_log2 - (m == -INFINITY ? 0.0f : m));
       for (int e = 0; e < 32; ++e) o[e] += p * __uint_as_float((uint32_t)a.pools.v[row + col + e] << 16);
     }

@@ -1278,3 +1278,23 @@ def test_append_records_sequences_without_a_token(cu):
     with pytest.raises(mk.MkError) as e:
         mk.check_status(st)
     assert e.value.code == mk.MK_ERR_DEVICE and "kv_append" in str(e.value)
+
+
+def test_attn_odd_values_in_a_long_run_end_in_time():
+    """A NaN among 40000 new tokens, each of which may lie outside a row's window: what it adds to the rows that see it is
+    found within the kernel's wait limits."""
+    g = gen(98)
+    n, W, P, d = 40001, 20000, 64, 64
+    assert math.gcd(7, n) == 1
+    pg = Paged(g, [n], 1, P, d)
+    q = torch.randn(n, 2, d, generator=g, device=DEV).to(BF)
+    pos = torch.arange(n, device=DEV) * 7 % n
+    st = new_status()
+    kw = dict(window=W, positions=pos.to(torch.int32), status=st)
+    clean, clean_lse = run_attn(pg, q, [0], [n], **kw)
+    j = 20011
+    pg.v[0, pg.tables[0, j // P].item(), :, j % P] = math.nan
+    out, lse = run_attn(pg, q, [0], [n], **kw)
+    mk.check_status(st)
+    see = (torch.arange(n, device=DEV) >= j) & (pos - pos[j] < W)
+    assert out[see].isnan().all() and torch.equal(out[~see], clean[~see]) and torch.equal(lse, clean_lse)
