@@ -1298,3 +1298,137 @@ def test_attn_odd_values_in_a_long_run_end_in_time():
     mk.check_status(st)
     see = (torch.arange(n, device=DEV) >= j) & (pos - pos[j] < W)
     assert out[see].isnan().all() and torch.equal(out[~see], clean[~see]) and torch.equal(lse, clean_lse)
+
+
+# ------------------------------------------------------- beside the decode step
+
+def decode_setup(shape, seed, batch, max_len):
+    import parity
+    model = parity._device_model(shape, seed, None)
+    return mk.Session(model, mk.Sched(model, batch, max_len))
+
+
+@pytest.mark.parametrize("R,W", [(1, 2), (2, 4)])
+def test_beam_search_over_the_decode_step(R, W):
+    """mk_decode_step, beam_select and beam_reorder, step after step: each surviving beam's cache and logits are those of its
+    own history, decoded again without any reordering."""
+    import synth
+    import synth.device
+    sh, seed = synth.MODELS["tiny"], 5
+    P, V, B, prompt, steps = sh.page_size, sh.vocab, R * W, 37, 21
+    cols, full = (prompt + steps + P - 1) // P, prompt // P
+    pages = R * full + B * (cols - full)
+    kp, vp = synth.device.device_pools(sh, seed, pages + B * cols)
+    ids = torch.randperm(pages + B * cols, generator=torch.Generator().manual_seed(seed)).tolist()
+    rows, again = [], [[ids.pop() for _ in range(cols)] for _ in range(B)]
+    for r in range(R):
+        common = [ids.pop() for _ in range(full)]
+        rows += [common + [ids.pop() for _ in range(cols - full)] for _ in range(W)]
+    for b in range(B):  # the prompt's rows (the generator's values), the same for the beams of a request
+        for c in range(full + 1):
+            for pool in (kp, vp):
+                if c == full and b % W:
+                    pool[:, rows[b][c]] = pool[:, rows[b - b % W][c]]
+                pool[:, again[b][c]] = pool[:, rows[b][c]]
+    cache = mk.KvCache(kp, vp, sh.rope_base)
+    sess, st = decode_setup(sh, seed, B, prompt + steps), new_status()
+    tables, again = [ints(rows), torch.empty(B, cols, dtype=torch.int32, device=DEV)], ints(again)
+    logits, ws = torch.empty(B, V, device=DEV), torch.empty(mk.beam_select_workspace_bytes(R, W, V, W), dtype=torch.uint8, device=DEV)
+    scores = torch.full((R, W), -math.inf, device=DEV)
+    scores[:, 0] = 0
+    out = [torch.empty(R, W, device=DEV), ints([[0] * W] * R), ints([[0] * W] * R)]
+    hist = [[[7 + r]] * W for r in range(R)]
+    tokens, moved = ints([h[-1] for row in hist for h in row]), 0
+    for t in range(steps):
+        n = prompt + t  # tokens in the caches before this step's
+        sess.step(tokens, ints([n + 1] * B), tables[0], kp, vp, logits)
+        sess.check()
+        if t + 1 == steps:
+            break
+        spiced = logits + 0.7 * torch.randn(B, V, generator=gen(100 + t), device=DEV)  # so that beams die and multiply
+        mk.beam_select(spiced, scores, *out, ws)
+        mk.beam_reorder(cache, ints([n + 1] * R), out[1], tables[0], tables[1], status=st)
+        tables.reverse()
+        parents = out[1].tolist()
+        moved += sum(len(set(p)) < W for p in parents)
+        hist = [[hist[r][p] + [w] for p, w in zip(parents[r], out[2].tolist()[r])] for r in range(R)]
+        tokens = out[2].flatten().clone()
+        scores.copy_(out[0])
+    mk.check_status(st)
+    assert moved > 4
+    want = torch.empty_like(logits)
+    for t in range(steps):
+        sess.step(ints([h[t] for row in hist for h in row]), ints([prompt + t + 1] * B), again, kp, vp, want)
+        sess.check()
+    # two runs of the step on the same history: fp32 sums in any order, K and V rounded to bf16 behind them
+    assert ((logits - want).abs() <= 1e-3 * want.abs().amax(-1, keepdim=True)).all()
+    s = torch.arange(prompt + steps, device=DEV)
+    for b in range(B):
+        for pool in (kp.view(BF), vp.view(BF)):
+            a, c = (pool[:, tab[b].long()[s // P], :, s % P].double() for tab in (tables[0], again))
+            assert torch.equal(a[:prompt], c[:prompt])
+            assert ((a - c).abs() <= c.abs() * 2.0 ** -7 + 1e-3 * c.abs().amax(-1, keepdim=True)).all(), b
+
+
+def test_append_rotates_as_the_decode_step():
+    """The step's K of one token at several positions against kv_append of its K at position 0, where nothing turns."""
+    import dataclasses
+
+    import synth
+    import synth.device
+    for name in ("tiny", "small"):
+        sh = dataclasses.replace(synth.MODELS[name], n_layers=1)
+        P, at = sh.page_size, [0, 1, 2, 77, 500, 1023]
+        cols = at[-1] // P + 1
+        kp, vp = synth.device.device_pools(sh, 3, 2 * cols)
+        tab = ints([list(range(cols)), list(range(cols, 2 * cols))])
+        sess = decode_setup(sh, 3, 1, at[-1] + 1)
+        cache, st = mk.KvCache(kp, vp, sh.rope_base), new_status()
+        logits = torch.empty(1, sh.vocab, device=DEV)
+        raw = None
+        for p in at:
+            sess.step(ints([11]), ints([p + 1]), tab[:1].contiguous(), kp, vp, logits)
+            sess.check()
+            k, v = (x.view(BF)[0, p // P, :, p % P].clone()[None] for x in (kp, vp))
+            if raw is None:
+                raw = k, v
+            mk.kv_append(cache, 0, *raw, ints([0, 1]), ints([p]), tab[1:].contiguous(), status=st)
+            got_k, got_v = (x.view(BF)[0, cols + p // P, :, p % P] for x in (kp, vp))
+            assert torch.equal(got_v, raw[1][0]) and torch.equal(v, raw[1])
+            # K at position 0 is rounded (2^-8 of either element of a pair), and each side's result; angles below 2^-20
+            mag = raw[0][0].double().abs().unflatten(-1, (-1, 2)).sum(-1, keepdim=True).expand(-1, -1, 2).flatten(-2)
+            assert ((got_k.double() - k[0].double()).abs() <= mag * (2.0 ** -8 + 2.0 ** -20) + 2 * plain.bf16_bound(k[0].double()) * 1.01).all(), p
+        mk.check_status(st)
+
+
+@pytest.mark.parametrize("lens", [[513, 1400], [512, 100], [1500]])
+def test_agrees_with_the_decode_steps_sliding_layers(lens):
+    """As test_agrees_with_the_decode_step, in a layer that sees a window of 512."""
+    import dataclasses
+
+    import synth
+    import synth.device
+    sh = dataclasses.replace(synth.MODELS["dense"], n_layers=1)
+    assert sh.window == 512 and not sh.is_full_layer(0)
+    B, P = len(lens), sh.page_size
+    need = [-(-n // P) for n in lens]
+    ids = torch.randperm(sum(need), generator=torch.Generator().manual_seed(4)).tolist()
+    bt = ints([[ids.pop() for _ in range(n)] + [-1] * (max(need) - n) for n in need])
+    kp, vp = synth.device.device_pools(sh, 4, sum(need))
+    sess, sl = decode_setup(sh, 4, B, max(lens)), ints(lens)
+    sess.step(ints([3 + 5 * b for b in range(B)]), sl, bt, kp, vp, torch.empty(B, sh.vocab, device=DEV))
+    sess.check()
+    q, attn = (sess.region(x, torch.float32, B * sh.n_q * sh.head_dim).view(B, sh.n_q, sh.head_dim) for x in ("q", "attn_out"))
+    cache, st = mk.KvCache(kp, vp, sh.rope_base), new_status()
+    qb = q.to(BF)
+    out = torch.empty_like(qb)
+    ws = torch.empty(mk.tree_attn_workspace_bytes(cache), dtype=torch.uint8, device=DEV)
+    mk.tree_attn(cache, 0, qb, out, ints(list(range(B + 1))), sl - 1, bt, ws, window=sh.window, status=st)
+    mk.check_status(st)
+    kc, vc = (x.view(BF)[0].cpu() for x in (kp, vp))
+    for b, n in enumerate(lens):
+        k, v = plain.gather_slots(kc, bt[b].tolist(), n), plain.gather_slots(vc, bt[b].tolist(), n)
+        ref, _, spread, size = plain.attention(q[b].cpu(), k, v, torch.arange(n) > n - 1 - sh.window, 1 / math.sqrt(sh.head_dim))
+        tol = plain.bf16_bound(ref) + spread * (2.0 ** -8 + 2 * size[:, None] * 2.0 ** -8)
+        assert ((out[b].cpu().double() - ref).abs() <= tol).all()
+        assert ((attn[b].cpu().double() - ref).abs() <= tol).all()
