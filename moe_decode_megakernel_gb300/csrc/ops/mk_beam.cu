@@ -314,6 +314,7 @@ struct Joined {
   Key2 next[kMaxOut];
   Key2 best[kThreads];
   Key2 tau, bound;
+  unsigned long long tied;  // the best score of a part's last kept logit that a neighbouring logit would have too
   int count;
 };
 
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
   const int per_row = parts * n, N = W * per_row;
   if (tid == 0) {
     k.count = 0;
+    k.tied = 0;
     k.tau = {0, 0};
   }
   wait_before();
@@ -445,7 +447,6 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
     const double s = (double)scores[w] + ((double)x - lse[w]);
     return s != s ? -INFINITY : s;
   };
-  uint64_t tied = 0;  // the best score of a part's last kept logit that a neighbouring logit would have too
   for (int base = 0; base < N; base += kTile) {
     Key2 key[kPer], b = {0, 0};
 #pragma unroll
@@ -469,15 +470,20 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
         if (q == 0) continue;
         token = (int)~(uint32_t)q;
         const uint32_t o = (uint32_t)(q >> 32);
-        score = score_of(w, unordered(o));
+        const float x = unordered(o);
+        const double off = (double)x - lse[w];
+        score = (double)scores[w] + off;
         // Of a part of more than n logits no other one scores above its last kept
         // one, and one that scores the same is of no account unless that is the
-        // last place's score and either of them has another logit.
-        if ((j + 1) % n == 0 && o > ordered(-INFINITY) &&
-            (score_of(w, just_below(o)) == score || score_of(w, just_above(o)) == score)) {
-          const uint64_t t = ordered64(score);
-          if (t > tied) tied = t;
+        // last place's score and either of them has another logit.  Neighbours of
+        // x differ by 2^-24 of its power of two or more, two roundings to 64 bits
+        // by 2^-50 of the larger result's: nearly always the exponents tell.
+        const int wide = max(__double2hiint(off) >> 20 & 0x7ff, __double2hiint(score) >> 20 & 0x7ff) - 1023;
+        if (wide - (int)((__float_as_uint(x) >> 23 & 0xff) - 127) >= 26 && o > ordered(-INFINITY) && (j + 1) % n == 0) {
+          score = score_of(w, x);
+          if (score_of(w, just_below(o)) == score || score_of(w, just_above(o)) == score) atomicMax(&k.tied, ordered64(score));
         }
+        if (score != score) score = -INFINITY;
       }
       key[i] = {ordered64(score), ~(uint32_t)(w * a.vocab + token)};
       if (above(key[i], b)) b = key[i];
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       }
     sort_out(k, n);
   }
-  if (__syncthreads_or(tied != 0 && k.count == n && tied == k.score[n - 1]))
+  if (k.tied != 0 && k.count == n && k.tied == k.score[n - 1])
     lowest_ties(a, k, done, scores, lse, top, score_of);
   for (int i = tid; i < n; i += kThreads) {
     const bool there = i < k.count;  // it is, unless an input changed between the kernels
