@@ -314,7 +314,6 @@ struct Joined {
   Key2 next[kMaxOut];
   Key2 best[kThreads];
   Key2 tau, bound;
-  unsigned long long tied;  // the best score of a part's last kept logit that a neighbouring logit would have too
   int count;
 };
 
@@ -350,14 +349,26 @@ __device__ __forceinline__ void sort_out(Joined& k, int n) {
 // continuations that score the same (by the whole block; all that score higher
 // are among the n, so the scores stay).  score(w, x): of logit x in beam w, top:
 // the beams' largest logits.  Only for scores above -inf, so beams without a
-// log-sum-exp have none.  It takes logits that differ by less than the last bit
-// of their score, 2^-52 of it: not made fast.
+// log-sum-exp have none.  The parts' keys tell first whether there is anything
+// to do: of a part of more than n logits no other one scores above its last kept
+// one, and one that scores the same is of no account unless that is the last
+// place's score and either of them has another logit.  It takes logits that
+// differ by less than the last bit of their score: not made fast.
 template <typename F>
-__device__ __noinline__ void lowest_ties(const SelectArgs& a, Joined& k, const bool* done, const float* scores,
+__device__ __noinline__ void settle_ties(const SelectArgs& a, Joined& k, const bool* done, const float* scores,
                                          const double* lse, const float* top, F score) {
   __shared__ int found[kWarps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = a.n_out;
   const uint64_t last = k.score[n - 1];
+  bool other = false;
+  for (int i = tid; i < a.beams * a.parts; i += kThreads) {
+    const int w = i / a.parts;
+    if (done[w] || lse[w] != lse[w]) continue;
+    const uint32_t o = (uint32_t)(a.keys[((int64_t)blockIdx.x * a.beams * a.parts + i) * n + n - 1] >> 32);
+    if (o > ordered(-INFINITY) && ordered64(score(w, unordered(o))) == last)
+      other |= ordered64(score(w, just_below(o))) == last || ordered64(score(w, just_above(o))) == last;
+  }
+  if (!__syncthreads_or(other)) return;
   int at = 0;
   while (k.score[at] > last) ++at;
   for (int w = 0; w < a.beams && at < n; ++w) {
@@ -404,7 +415,6 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
   const int per_row = parts * n, N = W * per_row;
   if (tid == 0) {
     k.count = 0;
-    k.tied = 0;
     k.tau = {0, 0};
   }
   wait_before();
@@ -469,21 +479,7 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
         const uint64_t q = base == 0 && i == 0 ? early : keys[c];
         if (q == 0) continue;
         token = (int)~(uint32_t)q;
-        const uint32_t o = (uint32_t)(q >> 32);
-        const float x = unordered(o);
-        const double off = (double)x - lse[w];
-        score = (double)scores[w] + off;
-        // Of a part of more than n logits no other one scores above its last kept
-        // one, and one that scores the same is of no account unless that is the
-        // last place's score and either of them has another logit.  Neighbours of
-        // x differ by 2^-24 of its power of two or more, two roundings to 64 bits
-        // by 2^-50 of the larger result's: nearly always the exponents tell.
-        const int wide = max(__double2hiint(off) >> 20 & 0x7ff, __double2hiint(score) >> 20 & 0x7ff) - 1023;
-        if (wide - (int)((__float_as_uint(x) >> 23 & 0xff) - 127) >= 26 && o > ordered(-INFINITY) && (j + 1) % n == 0) {
-          score = score_of(w, x);
-          if (score_of(w, just_below(o)) == score || score_of(w, just_above(o)) == score) atomicMax(&k.tied, ordered64(score));
-        }
-        if (score != score) score = -INFINITY;
+        score = score_of(w, unordered((uint32_t)(q >> 32)));
       }
       key[i] = {ordered64(score), ~(uint32_t)(w * a.vocab + token)};
       if (above(key[i], b)) b = key[i];
@@ -515,8 +511,18 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
       }
     sort_out(k, n);
   }
-  if (k.tied != 0 && k.count == n && k.tied == k.score[n - 1])
-    lowest_ties(a, k, done, scores, lse, top, score_of);
+  // Two logits of one score differ by less than the roundings on its way: from
+  // the last place's score back to a logit, whose neighbours are 2^-24 of its
+  // power of two away, nearly always the exponents tell that there are none (24:
+  // 2^-50 of the larger result for both roundings, a step of either exponent).
+  const uint64_t last = k.count == n ? k.score[n - 1] : 0;
+  bool near = false;
+  if (tid < W && last > ordered64(-INFINITY) && !done[tid] && lse[tid] == lse[tid]) {
+    const double t = unordered64(last), off = t - (double)scores[tid], x = off + lse[tid];
+    const auto power = [](double y) { return __double2hiint(y) >> 20 & 0x7ff; };
+    near = t == INFINITY || max(power(off), power(t)) - power(x) >= 24;
+  }
+  if (__syncthreads_or(near)) settle_ties(a, k, done, scores, lse, top, score_of);
   for (int i = tid; i < n; i += kThreads) {
     const bool there = i < k.count;  // it is, unless an input changed between the kernels
     const uint32_t c = there ? ~k.index[i] : 0;
