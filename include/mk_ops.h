@@ -133,8 +133,11 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
  * (unused rows of a page, masked tokens) does not reach its output, whatever
  * its bits.  Products of bf16 with fp32 sums; the running maximum, the sum
  * and the output are fp32, the probabilities are rounded to bf16 for the
- * product with V.  Pointers and strides multiples of 16 bytes.  Results do
- * not depend on timing: the same call gives the same bits.
+ * product with V.  (mk_decode_step keeps q, the probabilities and the output
+ * at fp32 accuracy: where two tokens are closer than bf16 tells, a draft that
+ * is verified here need not be the token that the step would have chosen.)
+ * Pointers and strides multiples of 16 bytes.  Results do not depend on timing:
+ * the same call gives the same bits.
  * A page id out of range is read as page 0; a sequence with a bad length, or
  * with more tokens than mask bits, is left out (its rows stay as they are); a
  * position out of range is moved into it.  All are recorded. */

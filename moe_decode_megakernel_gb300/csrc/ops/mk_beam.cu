@@ -11,9 +11,12 @@
 // are gone through once more (lowest_ties).
 //
 // Measured on a GB300: 64 requests of 8 beams over 65536 tokens (134 MB), the
-// best 16, 37 us: the first kernel 28 (4.8 TB/s, bound by its instructions:
-// some 150 for a warp's 512 logits and the bounds) and the second 9 (latency:
-// 64-bit logarithms and the ranks); 4 beams over 32768 tokens 12 us.
+// best 16, 34 us: the first kernel 27 (4.9 TB/s) and the second 7 (latency:
+// 64-bit logarithms and the ranks); 4 beams over 32768 tokens 12 us, 8 requests
+// of 8 beams over 65536 25.  The first kernel issues in half of its cycles: of
+// the 12 that a warp takes to an instruction it waits 3 for loads, 3 for earlier
+// results and 2 at the barriers of the bounds, and with 512 blocks on 152 SMs
+// (four on some, three on most) an SM is busy 77 % of the time.
 #include <cmath>
 
 #include "mk_ops_common.cuh"
@@ -533,8 +536,8 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
   }
 }
 
-// Parts of a row, whole tiles each: as many blocks as the GPU holds at once
-// (four per SM), no second wave.  A longer part is cheaper per logit, its bound
+// Parts of a row, whole tiles each: as many blocks as the GPU holds at once (four
+// per SM; three where n_out is above 32, so that some come second there).  A longer part is cheaper per logit, its bound
 // being nearer: 512 rows of 65536 logits took 38 us whole and 48, 63 and 56 us
 // in 2, 3 and 4 parts; 4 rows of 32768 fill 32 SMs in 8 parts.
 int parts_of(int64_t rows, int vocab) {

@@ -177,8 +177,8 @@ constexpr int kHeld = 8;    // rows a thread holds between their loads and store
 // it (the path ascends), so rows loaded before later places are written are
 // still the drafted ones.  No two threads touch the same bytes.  Bound by
 // latency at any real size (path, table and rows are three round trips to
-// memory): 32 sequences of up to five accepted tokens in 48 layers (8.7 MB) and
-// one sequence in eight layers both take 5 to 8 us.  A thread has eight rows
+// memory): behind another call, 32 sequences of up to five accepted tokens in 48
+// layers (11 MB) take 5.2 us and one sequence in eight layers 2.4.  A thread has eight rows
 // under way, so a path of eight costs what one of one does.
 __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitArgs a) {
   __shared__ int64_t from[kRound], to[kRound];  // rows of head 0, -1: nothing to do
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
 
 // Blocks of a request: its copies' (layer, K or V, head) units dealt evenly, so
 // that every child's copy keeps all of them equally busy, up to 4096 blocks in
-// all (three times what the GPU holds).  16 requests of 384 units: 192 blocks
+// all (three times what the GPU holds; above 512 requests eight each).  16 requests of 384 units: 192 blocks
 // each 50 us, 384 the same, 64, 128 and 256 took 56, 53 and 53; with nothing to
 // copy they take 13, 17 and, in 64 blocks, 9.  One request: 11 us, 21 in 64.
 unsigned reorder_blocks(int64_t requests, int64_t units) {
