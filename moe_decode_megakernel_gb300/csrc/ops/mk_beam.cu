@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(kThreads) select_join(const __grid_constant__ 
 }
 
 // Parts of a row, whole tiles each: as many blocks as the GPU holds at once (four
-// per SM; three where n_out is above 32, so that some come second there).  A longer part is cheaper per logit, its bound
-// being nearer: 512 rows of 65536 logits took 38 us whole and 48, 63 and 56 us
+// per SM; three where n_out is above 32, so that some come second there).  A
+// longer part is cheaper per logit, its bound being nearer: 512 rows of 65536 logits took 38 us whole and 48, 63 and 56 us
 // in 2, 3 and 4 parts; 4 rows of 32768 fill 32 SMs in 8 parts.
 int parts_of(int64_t rows, int vocab) {
   const int64_t tiles = (vocab + kTile - 1) / kTile;

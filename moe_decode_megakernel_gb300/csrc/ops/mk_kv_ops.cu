@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
 // that every child's copy keeps all of them equally busy, up to 4096 blocks in
 // all (three times what the GPU holds; above 512 requests eight each).  16 requests of 384 units: 192 blocks
 // each 50 us, 384 the same, 64, 128 and 256 took 56, 53 and 53; with nothing to
-// copy they take 13, 17 and, in 64 blocks, 9.  One request: 11 us, 21 in 64.
+// copy a call takes 7 us behind another.  One request: 11 us, 21 in 64.
 unsigned reorder_blocks(int64_t requests, int64_t units) {
   int64_t most = 4096 / requests;
   most = most < 8 ? 8 : most > 384 ? 384 : most;
