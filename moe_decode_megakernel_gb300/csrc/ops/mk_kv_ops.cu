@@ -353,9 +353,10 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
 
 // Blocks of a request: its copies' (layer, K or V, head) units dealt evenly, so
 // that every child's copy keeps all of them equally busy, up to 4096 blocks in
-// all (three times what the GPU holds; above 512 requests eight each).  16 requests of 384 units: 192 blocks
-// each 50 us, 384 the same, 64, 128 and 256 took 56, 53 and 53; with nothing to
-// copy a call takes 7 us behind another.  One request: 11 us, 21 in 64.
+// all (three times what the GPU holds; above 512 requests eight each).  16
+// requests of 384 units: 192 blocks each 50 us, 384 the same, 64, 128 and 256
+// took 56, 53 and 53; with nothing to copy a call takes 7 us behind another.
+// One request: 11 us, 21 in 64.
 unsigned reorder_blocks(int64_t requests, int64_t units) {
   int64_t most = 4096 / requests;
   most = most < 8 ? 8 : most > 384 ? 384 : most;
