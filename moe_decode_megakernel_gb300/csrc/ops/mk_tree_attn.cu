@@ -53,6 +53,7 @@
 #include <cmath>
 
 #include "mk_ops_mma.cuh"
+#include "mk_ops_parts.h"
 #include "mk_ops_tmem.cuh"
 
 namespace mk {
@@ -120,11 +121,6 @@ struct Item {
 struct Border {
   int64_t first, at;
   Item item;
-};
-
-// The first and the last CTA that an item's tiles were dealt to (each writes its own number).
-struct Placed {
-  int32_t first, last;
 };
 
 // A token as the joining kernel sees it: its sequence's first row and the sequence (-1: left
@@ -1517,12 +1513,13 @@ __global__ void __launch_bounds__(kJoinThreads* kShare) join_kernel(const __grid
 // a warp, from its group's item and its sequence's own; each of them lies as a
 // whole in seg_o, or in the parts of the CTAs that its tiles were dealt to.  A
 // row that has neither another item nor another part was written by the first
-// kernel.  Bound by latency: two round trips for the token and its items, one for
-// the first part of both, one for each kUnderWay further parts.  kShare 4, for
-// few tokens, whose parts are many: four warps share a quad's further parts and meet in
-// shared memory.
+// kernel; one whose items are nowhere (parts_of: a wait was given up, which is
+// recorded) stays as it is.  Bound by latency: two round trips for the token and
+// its items, one for the first part of both, one for each kUnderWay further
+// parts.  kShare 4, for few tokens, whose parts are many: four warps share a
+// quad's further parts and meet in shared memory.
 template <int D, int kShare>
-__global__ void __launch_bounds__(kJoinThreads) merge_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) merge_kernel(const __grid_constant__ AttnArgs a, int grid) {
   constexpr int kWarps = kJoinThreads / 32 / kShare, kUnderWay = kShare == 1 ? 6 : 4;
   __shared__ float2 meet_ml[kShare == 1 ? 1 : kWarps * kShare][32];
   __shared__ float4 meet_o[kShare == 1 ? 1 : kWarps * kShare][32];
@@ -1537,8 +1534,8 @@ __global__ void __launch_bounds__(kJoinThreads) merge_kernel(const __grid_consta
   const Placed own = a.placed[placed_at(a, 1, h, tok.b, tok.t0, r1)];
   Placed all = {0, -1};
   if (tok.group_b >= 0) all = a.placed[placed_at(a, 0, h, tok.group_b, tok.group_t0, r0)];
-  const int n0 = all.last - all.first + 1, n1 = own.last - own.first + 1;  // parts
-  const bool mine = head < a.n_q && (n0 > 0 || n1 > 1);
+  const int n0 = parts_of(all, grid), n1 = parts_of(own, grid);
+  const bool mine = head < a.n_q && (n0 > 0 ? n1 > 0 : n1 > 1 && tok.group_b < 0);
   if (kShare == 1 ? !__any_sync(FULL, mine) : !__syncthreads_or(mine)) return;
   const int share = warp / kWarps, col = blockIdx.z * kWarps + warp % kWarps;  // columns in fours
   float4 o = make_float4(0, 0, 0, 0);
@@ -1562,7 +1559,7 @@ __global__ void __launch_bounds__(kJoinThreads) merge_kernel(const __grid_consta
         ml[x] = a.seg_ml[x * all_rows + row];
         p[x] = a.seg_o[(x * (D / 4) + col) * all_rows + row];
       } else if (n > 1) {
-        const int64_t slot = 2 * (x ? own.first : all.first) + 1;
+        const int64_t slot = part_slot(x ? own : all, 0);
         ml[x] = a.part_ml[slot * kRows + (x ? r1 : r0) % kRows];
         p[x] = a.part_o[(slot * (D / 4) + col) * kRows + (x ? r1 : r0) % kRows];
       }
@@ -1574,7 +1571,7 @@ __global__ void __launch_bounds__(kJoinThreads) merge_kernel(const __grid_consta
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int n = mine ? x ? n1 : n0 : 0, r = (x ? r1 : r0) % kRows;
-    const int64_t slot = 2 * ((x ? own.first : all.first) + 1 + share);
+    const int64_t slot = part_slot(x ? own : all, 1 + share);
     const float2* pml = a.part_ml + slot * kRows + r;
     const float4* po = a.part_o + (slot * (D / 4) + col) * kRows + r;
     constexpr int kStep = 2 * kShare;  // slots from part to part
@@ -1639,8 +1636,8 @@ int launch_shared(const AttnArgs& a, int grid, cudaStream_t st) {
   rc = launch("prefix_attn", attn_kernel<D, true>, dim3(grid), kThreads, smem, st, a);
   if (rc != MK_OK) return rc;
   const unsigned T = (unsigned)a.b.n_tokens, heads = (unsigned)(a.n_q + 31) / 32;
-  if ((int64_t)T * heads <= kFew) return launch("prefix_attn", merge_kernel<D, 4>, dim3(T, heads, D / 8), kJoinThreads, 0, st, a);
-  return launch("prefix_attn", merge_kernel<D, 1>, dim3(T, heads, D / 32), kJoinThreads, 0, st, a);
+  if ((int64_t)T * heads <= kFew) return launch("prefix_attn", merge_kernel<D, 4>, dim3(T, heads, D / 8), kJoinThreads, 0, st, a, grid);
+  return launch("prefix_attn", merge_kernel<D, 1>, dim3(T, heads, D / 32), kJoinThreads, 0, st, a, grid);
 }
 
 template <int D>
