@@ -382,8 +382,9 @@ __device__ __forceinline__ uint32_t s_cols(int w, int buf) { return (w * 2 + buf
 // in turn.  By a warp for each group: the waits and the issue of a step take
 // about as long as its MMAs, one warp for both left the tensor cores idle half
 // of the time.  The lanes leave every wait together, and every tile of the ring
-// is waited for in order, the other group's too: a warp that skipped phases of a
-// barrier could wait for its parity for good.
+// is waited for in order, the other group's too, and handed back by both warps:
+// one that skipped phases of a barrier, or that a refilled stage overtook, could
+// wait for its parity for good.
 template <int D, int kQ>
 __device__ __forceinline__ bool issue_mmas(const MassArgs& a, uint8_t* smem, Ctl& c, const int w) {
   using G = Geo<D, kQ>;
@@ -425,6 +426,8 @@ __device__ __forceinline__ bool issue_mmas(const MassArgs& a, uint8_t* smem, Ctl
             ++step;
           }
           commit_if(lead, empty + k.stage * 8);
+        } else {
+          arrive_if(lead, empty + k.stage * 8);
         }
         k.advance<G::kStages>();
       }
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       c.abort = 0;
       for (int i = 0; i < G::kStages; ++i) {
         mbar_init(&c.full[i], 1);
-        mbar_init(&c.empty[i], 1);
+        mbar_init(&c.empty[i], 2);
       }
       for (int i = 0; i < 4; ++i) {
         mbar_init(&c.s_full[i / 2][i % 2], 1);
