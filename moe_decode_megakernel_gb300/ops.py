@@ -274,7 +274,8 @@ def kv_append_norm(cache: KvCache, layer: int, k, v, cu_seqlens, cache_lens, blo
         _dims(axis_positions, "axis_positions", 2)
         axes = _int32(axis_positions.shape[0], "axes")
         try:
-            ax = bytes(pair_axis) if len(pair_axis) == d // 2 else b""  # read before the call returns
+            # read before the call returns; element by element: an array gives bytes() its storage
+            ax = bytes(list(pair_axis)) if len(pair_axis) == d // 2 else b""
         except (TypeError, ValueError):
             ax = b""
         if not ax or max(ax) >= axes:

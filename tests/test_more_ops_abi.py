@@ -235,3 +235,50 @@ def test_binding_refuses():
 
     for shape in (((1 << 32) + 1, 4, 1), (1, 1 << 32, 1), (1, 4, (1 << 32) + 1), (-1, 4, 1)):
         assert ops.prefix_attn_workspace_bytes(c, *shape) == 0
+
+
+def pair_axes():
+    import array
+
+    import numpy as np
+    import torch
+    a = [0] * 12 + [1] * 10 + [2] * 10
+    return {"list": a, "tuple": tuple(a), "bytes": bytes(a), "bytearray": bytearray(a), "array": array.array("i", a),
+            "array of 64 bits": array.array("q", a), "int64": np.array(a), "int32": np.array(a, np.int32),
+            "uint8": np.array(a, np.uint8), "strided": np.repeat(np.array(a, np.int16), 2)[::2], "tensor": torch.tensor(a),
+            "tensor of bytes": torch.tensor(a, dtype=torch.uint8), "numbers": [np.int64(x) for x in a]}
+
+
+@pytest.mark.parametrize("kind", pair_axes())
+def test_binding_passes_axes_whatever_holds_them(kind, monkeypatch):
+    """pair_axis are whole numbers, not the bytes that an array keeps them in."""
+    import torch
+
+    class Fake:
+        device, n_layers, n_kv, head_dim, handle = torch.device("cpu"), 2, 2, 64, None
+    got = []
+
+    def call(fn, device, stream, *args):
+        norm = next(x for x in args if isinstance(x, ops.MkHeadNorm))
+        got.append((ctypes.string_at(norm.pair_axis, 32), norm.n_axes))
+
+    ops._lib()
+    monkeypatch.setattr(ops, "_call", call)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(4, 2, 64)
+    mk.kv_append_norm(Fake(), 0, k, k.clone(), i(3), i(2), i(2, 4), axis_positions=i(3, 4), pair_axis=pair_axes()[kind])
+    assert got == [(bytes([0] * 12 + [1] * 10 + [2] * 10), 3)]
+
+
+def test_binding_refuses_axes_that_are_no_whole_numbers():
+    import numpy as np
+    import torch
+
+    class Fake:
+        device, n_layers, n_kv, head_dim, handle = torch.device("cpu"), 2, 2, 64, None
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(4, 2, 64)
+    ops._lib()
+    for bad in (np.zeros(32), np.zeros(32, np.float16), np.zeros((32, 2), np.int64), np.full(32, 3), np.full(32, -1),
+                np.full(32, 256), torch.zeros(32), "0" * 32, 32):
+        assert refused(mk.kv_append_norm, Fake(), 0, k, k.clone(), i(3), i(2), i(2, 4), axis_positions=i(3, 4), pair_axis=bad), bad
