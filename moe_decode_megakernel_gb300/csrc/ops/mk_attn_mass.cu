@@ -65,6 +65,10 @@ constexpr int kThreads = 384;
 constexpr int kOpening = 15;             // units of a tile's cost
 constexpr int kItems = 4;                // runs planned ahead
 constexpr int64_t kWaitNs = 2000000000;  // a wait that takes longer is given up
+// The planning warp's, which lasts as long as a run does (a prompt of 2^19 tokens
+// over 2^20 slots takes seconds); where a role is stuck its own wait, of a tile or
+// a block, ends all of them.
+constexpr int64_t kPlanNs = 60 * kWaitNs;
 
 template <int D, int kQ>
 struct Geo {
@@ -212,8 +216,8 @@ __device__ __forceinline__ Rows rows_of(const MassArgs& a, const Item& it, int q
 
 // Waits for a phase; false when this wait, or another one of the CTA, has
 // taken too long.
-__device__ __forceinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
-  const int64_t until = gtimer() + kWaitNs;
+__device__ __forceinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status, int64_t limit) {
+  const int64_t until = gtimer() + limit;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (ld_volatile(&c.abort)) return false;
@@ -225,8 +229,8 @@ __device__ __forceinline__ bool wait_slow(Ctl& c, uint64_t* bar, uint32_t parity
   }
 }
 // By a whole warp, whose lanes leave every wait together.
-__device__ __forceinline__ bool wait(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return __all_sync(FULL, mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, status)) != 0;
+__device__ __forceinline__ bool wait(Ctl& c, uint64_t* bar, uint32_t parity, uint32_t* status, int64_t limit = kWaitNs) {
+  return __all_sync(FULL, mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, status, limit)) != 0;
 }
 
 // The plan is made by one warp and handed to the others through shared memory,
@@ -238,7 +242,7 @@ __device__ __forceinline__ bool plan(const MassArgs& a, Ctl& c) {
   uint32_t n = 0;
   auto give = [&](const Item& it) {
     const int s = n % kItems;
-    if (n >= kItems && !wait(c, &c.taken[s], (n / kItems - 1) & 1, a.status)) return false;
+    if (n >= kItems && !wait(c, &c.taken[s], (n / kItems - 1) & 1, a.status, kPlanNs)) return false;
     if (threadIdx.x % 32 == 0) {
       c.items[s] = it;
       mbar_arrive(&c.planned[s]);
