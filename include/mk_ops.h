@@ -121,6 +121,8 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
  * and rotations by several positions: pair i of a head (elements 2i and 2i +
  * 1) is turned by axis_positions[pair_axis[i]][t] * rope_base^(-2i /
  * head_dim).  fp32 throughout, rounded once to bf16; v is rounded only.
+ * (mk_decode_step knows neither norms nor axes: what follows such tokens is
+ * appended by this call and attended by those below.)
  *  eps        > 0 (a normal fp32 number): the heads of q and k are normalised;
  *             0: they are not, and there are no gains
  *  q_gain, k_gain  device fp32 [head_dim], 16-byte aligned, the same for
@@ -231,6 +233,9 @@ int mk_prefix_attn(mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_attn
  *             tokens; -inf: the token's row counts for nothing
  *  mass       device fp32 [batch][n_kv][mass_stride]; apart from the inputs
  *  decay      0 to 1
+ * Each slot is read through its own sequence's row of the tables: where
+ * sequences share a prefix their rows name its pages too, and a page in which a
+ * prefix ends holds its rows in each of them (mk_prefix_attn reads neither).
  * What a token does not see counts 0, whatever its bits.  Products of bf16 with
  * fp32 sums; exponentials and sums are fp32, in an order of their own: the same
  * call gives the same bits.
@@ -268,12 +273,14 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
  * keep[b]) of its lens[b] slots: the first `sinks`, the last `recent`, and
  * between them those of the largest mass (of equal ones the lower slot; what is
  * not a number counts as -inf).  Their K and V move, in order, to its first slots.
+ * As for mk_attn_mass, a sequence's row of the tables names the pages of all its slots.
  *  lens, keep  device int32 [batch]
  *  out_tables  device int32 [batch][max_pages]: the pages that the kept slots move
  *             to; NULL: block_tables, the slots move within their own pages.  A
  *             column names either the page of the same column of block_tables or a page that
  *             block_tables does not name and no other column of out_tables does
- *             (sequences that share pages are given new ones)
+ *             (sequences that share pages are given new ones: in place
+ *             each of them would move its own slots within the others' pages, without a record)
  *  mass       device fp32 [n_layers][batch][n_kv][mass_stride], as mk_attn_mass
  *             sums it up layer by layer
  *  mass_out   the masses of the kept slots in their new order, the same shape; mass
@@ -284,6 +291,9 @@ int mk_kv_commit(const mk_kv* kv, int32_t batch, const int32_t* cache_lens, cons
  * The tables serve all layers and heads, a slot now holds tokens of different
  * positions in each: the rotation has been applied to K, so attention without a
  * window is not concerned, and new tokens are appended by mk_tokens.positions.
+ * mk_decode_step does not go on with such a cache: it turns a new token by its
+ * slot, which no longer is its position, and its layers with a window take slots
+ * for positions, without a record.
  * A sequence with a length beyond its table or mass_stride, with keep below
  * sinks + recent (and below its length), or with more than max_keep to keep is
  * left out (its new length is its length); a copy from or to a page out of range is left out.

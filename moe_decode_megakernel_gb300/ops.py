@@ -10,7 +10,8 @@ argument marshalling only, on torch-owned device memory.
     prefix_attn(cache, layer, q_out, out, cu_seqlens, cache_lens, block_tables, group_seqs, prefix_lens, workspace)
     attn_mass(cache, layer, q_out, lse, mass, cu_seqlens, cache_lens, block_tables, tree_mask=mask, positions=pos)
     kv_commit(cache, cache_lens, path, path_lens, block_tables, new_lens=new_lens)
-    kv_evict(cache, lens, keep, mass, kept, block_tables, mass_out=mass, new_lens=new_lens, sinks=4, recent=64)
+    kv_evict(cache, lens, keep, mass, kept, block_tables, out_tables=own_tables, mass_out=mass, new_lens=new_lens,
+             sinks=4, recent=64)  # without out_tables in place: for sequences that share no page
     beam_select(logits, scores, out_scores, out_parents, out_tokens, workspace)
     beam_reorder(cache, lens, parents, tables_in, tables_out)
 
@@ -352,7 +353,8 @@ def attn_mass(cache: KvCache, layer: int, q, lse, mass, cu_seqlens, cache_lens, 
               stream=None) -> None:
     """mk_attn_mass: q, tree_mask, positions, window and scale as for
     tree_attn, lse fp32 [tokens][n_q] as it gave it; mass fp32
-    [batch][n_kv][slots]."""
+    [batch][n_kv][slots].  block_tables name every page of each sequence, those
+    of a shared prefix too."""
     dev, f32 = cache.device, torch.float32
     _dims(q, "q", 3)
     _dims(mass, "mass", 3)
@@ -390,7 +392,9 @@ def kv_evict(cache: KvCache, lens, keep, mass, kept, block_tables, out_tables=No
              sinks: int = 0, recent: int = 0, status=None, stream=None) -> None:
     """mk_kv_evict: lens and keep int32 [batch], mass (and mass_out) fp32
     [layers][batch][n_kv][slots], kept int32 [layers][batch][n_kv][max_keep],
-    tables int32 [batch][max_pages]."""
+    tables int32 [batch][max_pages].  Sequences that share pages need out_tables
+    of their own; a cache that was cut down is not for mk_decode_step, which
+    takes slots for positions."""
     dev, i32, f32 = cache.device, torch.int32, torch.float32
     _dims(lens, "lens", 1)
     _dims(mass, "mass", 4)
