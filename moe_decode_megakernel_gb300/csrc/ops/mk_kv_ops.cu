@@ -21,7 +21,7 @@ constexpr int kThreads = 256;
 // slot is known (its sequence, then its page: two round trips to memory); the
 // thread whose sequence holds the token looks the slot up, half a head of
 // threads turns the position into sines.  12.6K tokens of 40 heads of 128 (258 MB moved) take 42
-// us, 6.2 TB/s where a copy of that size reaches 6.8: bound by memory.  Small
+// us, 6.2 TB/s where a copy of that size reaches 6.7: bound by memory.  Small
 // blocks with many chunks of a thread under way: 256 threads with three took 48
 // us, 128 with three 44; 64 with ten were no faster.
 // Eight tokens are a chain of four round trips, 3 us behind another kernel.  The

@@ -38,11 +38,11 @@
 //
 // Measured on a GB300 (heads of 128, 8 query heads to a K/V head, BF16): 32
 // trees of up to 16 tokens over 512 to 32K slots 182 us, 1.09 GB of K and V at
-// 6.0 TB/s (a copy: 6.8), bound by memory; 2048 tokens of a run over 8K slots
-// 219 us, 1.41 PFLOP/s (cuBLAS: 1.9), the tensor pipe active 64% of the
+// 6.0 TB/s (a copy: 6.7), bound by memory; 2048 tokens of a run over 8K slots
+// 217 us, 1.42 PFLOP/s (cuBLAS: 1.9), the tensor pipe active 65% of the
 // kernel's cycles, bound by the hand-overs between exponentials and MMAs (a
-// step of 64 slots takes a group some 1650 cycles, of which its own and the
-// other group's MMAs run 1024); eight tokens over 8K slots 17 us: 2.6 the
+// step of 64 slots takes a group some 1570 cycles, its share of plan and
+// openings among them, of which its own and the other group's MMAs run 1024); eight tokens over 8K slots 17 us: 2.6 the
 // plan, 6 two tiles and the output, 2 to end and begin a kernel, 4 the join.
 // Shared prefixes: 64 sequences of one token over 32K shared and 50 to 2000 own
 // slots 73 us (7 to the plan, 46 of tiles and openings on average, 54 at most, 8
