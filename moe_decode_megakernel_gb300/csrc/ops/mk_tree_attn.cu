@@ -285,13 +285,20 @@ __device__ __forceinline__ Part part_at(const AttnArgs& a, const Group& mine, in
   return p;
 }
 
-// The token of a query row of a sequence (the first and the last, which most plans ask for, without a division).
+// The token of a query row of a sequence.  kFew: the first and the last, which
+// plans of single tokens ask for, without a division (1024 of them over 1K slots
+// 505 us, 513 with it); not where the lanes of a warp ask for rows of different
+// kinds and would go through all the branches (200 prompts of 40 tokens over up
+// to 300 slots 169 us, 156 without).
+template <bool kFew>
 __device__ __forceinline__ int token_of(const AttnArgs& a, const Part& s, int row) {
-  return row == 0 ? 0 : row == s.n * a.group - 1 ? s.n - 1 : (int)((uint32_t)row / (uint32_t)a.group);
+  if (kFew && row == 0) return 0;
+  if (kFew && row == s.n * a.group - 1) return s.n - 1;
+  return (int)((uint32_t)row / (uint32_t)a.group);
 }
 
 // Tiles [lo, hi) of query group m of a sequence.
-template <bool kShared>
+template <bool kShared, bool kFew = true>
 __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Part& s, int m, int& lo, int& hi) {
   if (kShared && s.from == kPrefix) {  // no token's position is below the prefix
     hi = (s.ctx + kTile - 1) / kTile;
@@ -301,7 +308,7 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Part& s, int m
     return;
   }
   const int all = s.n * a.group, r0 = m * kRows, r1 = all - r0 < kRows ? all : r0 + kRows;  // below 2^31
-  const int i0 = a.mask ? 0 : token_of(a, s, r0), i1 = a.mask ? 0 : token_of(a, s, r1 - 1);
+  const int i0 = a.mask ? 0 : token_of<kFew>(a, s, r0), i1 = a.mask ? 0 : token_of<kFew>(a, s, r1 - 1);
   const int end = s.ctx + (a.mask ? s.n : i1 + 1);
   hi = (end + kTile - 1) / kTile;
   lo = kShared ? s.from / kTile : 0;
@@ -363,7 +370,7 @@ __device__ __forceinline__ Load load_of(const AttnArgs& a, const Group& mine, in
     const Part q = part_from<kShared>(x.s, src);
     int64_t u = 0, big = 0;
     for (int m = lane, n = groups_of(a, q); m < n; m += 32) {
-      tiles_of<kShared>(a, q, m, lo, hi);
+      tiles_of<kShared, false>(a, q, m, lo, hi);
       u += hi - lo;
       if (kShared && is_big(a, q, m)) big += hi - lo;
     }
@@ -450,7 +457,7 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Part& s, int 
     it.window_to = a.window ? s.ctx : 0;  // the sequences' own lengths say which
     return it;
   }
-  const int i0 = token_of(a, s, it.row0), i1 = token_of(a, s, it.row0 + it.rows - 1);
+  const int i0 = token_of<false>(a, s, it.row0), i1 = token_of<false>(a, s, it.row0 + it.rows - 1);
   // without a mask every row sees the new tokens up to the first row's own,
   // unless positions set them a window or more apart
   const bool apart = a.window && a.b.positions && s.n > a.window;
@@ -490,7 +497,7 @@ __device__ __forceinline__ void each_item(const AttnArgs& a, const Group& mine, 
           bool found = false;
           for (m = 0; m < M && !found; m += 32) {
             int lo = 0, hi = 0;
-            if (m + lane < M) tiles_of<kShared>(a, q, m + lane, lo, hi);
+            if (m + lane < M) tiles_of<kShared, false>(a, q, m + lane, lo, hi);
             const int64_t n = m + lane < M ? (hi - lo) * weight<kShared>(a, c, q, m + lane) + c.opening : 0, sum = warp_scan(n);
             const uint32_t past = __ballot_sync(FULL, m + lane < M && at + skipped + sum > u);
             found = past != 0;
