@@ -122,7 +122,9 @@ int mk_kv_append(const mk_kv* kv, int32_t layer, const mk_tokens* tok, const mk_
  * 1) is turned by axis_positions[pair_axis[i]][t] * rope_base^(-2i /
  * head_dim).  fp32 throughout, rounded once to bf16; v is rounded only.
  * (mk_decode_step knows neither norms nor axes: what follows such tokens is
- * appended by this call and attended by those below.)
+ * appended by this call and attended by those below.  With neither, its products
+ * round in another order than mk_kv_append's: a last place of fp32, seldom one of
+ * bf16.)
  *  eps        > 0 (a normal fp32 number): the heads of q and k are normalised;
  *             0: they are not, and there are no gains
  *  q_gain, k_gain  device fp32 [head_dim], 16-byte aligned, the same for
